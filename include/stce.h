@@ -77,10 +77,14 @@ extern "C" {
 typedef enum {
   STCE_DT_BF16 = 1, /* hidden and weight are bf16 (the fast path) */
   STCE_DT_F32 = 2,  /* hidden and weight are fp32 */
-  STCE_DT_FP8 = 3   /* the fp8 lane: weight of e4m3 codes [V, H] (uint8) with
+  STCE_DT_FP8 = 3,  /* the fp8 lane: weight of e4m3 codes [V, H] (uint8) with
                        per-row fp32 scales stce_problem.weight_scale; hidden
                        bf16 [T, H], quantized per row by the library; H a
                        multiple of 16 */
+  STCE_DT_F16 = 4 /* fp16: logits, quantizer inputs and product outputs of the
+                     operators on given arrays (stce_token_logprobs,
+                     stce_fp8_quantize_blocks, stce_fp8_block_matmul); the
+                     scoring core does not take it */
 } stce_dtype;
 
 typedef enum {
@@ -407,6 +411,11 @@ stce_status stce_decode_state(const void *host_state, int64_t nrows, stce_row_in
 #define STCE_KERNEL_TILE_LISTS 18  /* backward: per-tile lists of the rows whose keys are recomputed there */
 #define STCE_KERNEL_TILE_RECOMPUTE 19 /* backward: recompute of those rows' keys on their listed tiles */
 #define STCE_KERNEL_LISTED_ENTRIES 20 /* backward: dz entries of the rows whose support the state lists */
+#define STCE_KERNEL_TOKEN_LOGPROBS 21 /* token logprobs: statistics and alternatives of rows or row segments */
+#define STCE_KERNEL_TOKEN_MERGE 22    /* token logprobs: rows joined from their segments */
+#define STCE_KERNEL_TOKEN_GRAD 23     /* token logprobs: gradient of the logits */
+#define STCE_KERNEL_QUANTIZE_BLOCKS 24 /* e4m3 quantization with a scale per block of 128 */
+#define STCE_KERNEL_BLOCK_MATMUL 25   /* block-scaled fp8 product */
 typedef struct stce_profile {
   int32_t capacity;
   int32_t count;
@@ -523,6 +532,125 @@ stce_status stce_fused_policy_step(const stce_problem *prob, const stce_pg_param
  * Enqueued on `stream`; host errors as stce_forward.  R = 0 does nothing. */
 stce_status stce_fp8_quantize_rows(const void *x, int64_t R, int64_t H, uint8_t *codes, float *scales,
                                    void *stream);
+
+/* Log probabilities of given tokens under given logits, with the rows'
+ * log-sum-exp, entropy and top alternatives (no sampling program: the whole
+ * row is the support).  For logits z [T, V], s = z / temperature per row:
+ *   lse[t]          = logsumexp_j s[t, j]
+ *   logprob[t, i]   = min(s[t, tokens[t, i]] - lse[t], 0)
+ *   entropy[t]      = -sum_j p_j log p_j, p = softmax(s[t, :]), in nats
+ *   top_id[t, n], top_logprob[t, n]: the top_n tokens with the largest
+ *                     logits, in decreasing order, the lower id first among
+ *                     equal logits (-0 and +0 are equal).
+ * A logit of -inf is a masked token: probability 0, logprob -inf, never an
+ * alternative; places past a row's last unmasked token (and past V) hold id
+ * -1 and logprob -inf.  A row with every token masked has lse and logprobs
+ * -inf and entropy 0.  A row that holds a NaN or +inf, or whose temperature
+ * is not finite and > 0, has NaN outputs and alternatives of id -1 and NaN.
+ * With STCE_PROBLEM_IGNORE_INDEX a token equal to ignore_index scores 0; any
+ * other token outside [0, V) scores NaN.  Invalid temperatures and tokens are
+ * reported in *dev_status as stce_forward does (STCE_FIELD_TEMPERATURE,
+ * STCE_FIELD_TARGET).
+ * Logits are read once; the row maximum, sums and entropy are fp32 (the
+ * exponentials taken relative to the running maximum). */
+typedef struct stce_token_problem {
+  int64_t T;      /* rows, 0 <= T <= 2^24 (0: nothing is done) */
+  int64_t V;      /* tokens per row, 1 <= V < 2^31 - 512 */
+  int32_t dtype;  /* of the logits: STCE_DT_BF16, STCE_DT_F16 or STCE_DT_F32 */
+  int32_t flags;  /* 0 or STCE_PROBLEM_IGNORE_INDEX */
+  const void *logits; /* [T, V], row stride ld elements, aligned to an element */
+  int64_t ld;     /* >= V */
+  const float *temperature; /* [T] finite > 0, or NULL = 1 */
+  const int64_t *tokens;    /* [T, K] token ids (NULL with K = 0) */
+  int32_t K;      /* given tokens per row, 0 <= K <= 1024 */
+  int32_t top_n;  /* alternatives per row, 0 <= top_n <= 128 */
+  int64_t ignore_index; /* with STCE_PROBLEM_IGNORE_INDEX, outside [0, V) */
+} stce_token_problem;
+/* Device arrays; NULL = not wanted.  stats [T, 4] fp32 is what the backward
+ * reads: the row's largest logit (as it stands, not divided by the
+ * temperature), the log of the sum of exp((z - largest) / temperature), the
+ * entropy, and 0; NaN in all four for an invalid row.  16-byte aligned. */
+typedef struct stce_token_outputs {
+  float *logprob;     /* [T, K] */
+  float *lse;         /* [T] */
+  float *entropy;     /* [T] */
+  float *top_logprob; /* [T, top_n] */
+  int64_t *top_id;    /* [T, top_n] */
+  float *stats;       /* [T, 4] */
+} stce_token_outputs;
+/* Workspace bytes of stce_token_logprobs (0 when every row is one
+ * workgroup's): the partial statistics and alternatives of the row segments
+ * when few rows are split over many workgroups.  Pointers are not read. */
+stce_status stce_token_workspace_bytes(const stce_token_problem *prob, size_t *bytes);
+stce_status stce_token_logprobs(const stce_token_problem *prob, const stce_token_outputs *out, int64_t *dev_status,
+                                void *ws, size_t ws_bytes, void *stream);
+
+/* Gradient of sum_t (sum_i grad_logprob[t, i] logprob[t, i] + grad_entropy[t]
+ * entropy[t] + grad_lse[t] lse[t]) with respect to the logits:
+ *   dz[t, j] = (1 / T_t) (sum_i g_i 1[j = y_i]
+ *              + p_j (grad_lse - sum_i g_i - grad_entropy (log p_j + H)))
+ * with p, H from `stats` (the forward's) and the logits.  A given token that
+ * is masked (logit -inf), ignored or outside [0, V) passes no gradient; a
+ * token given twice passes the sum of both.  The gradients of masked rows and
+ * of invalid rows are zero.  grad_logprob [T, K], grad_entropy [T] and
+ * grad_lse [T] may each be NULL (no such term).  Writes grad_logits [T, V] in
+ * the logits' dtype, row stride ld_grad; it must not overlap the logits.
+ * prob->top_n is not read.  No workspace. */
+stce_status stce_token_logprobs_backward(const stce_token_problem *prob, const float *stats,
+                                         const float *grad_logprob, const float *grad_entropy,
+                                         const float *grad_lse, void *grad_logits, int64_t ld_grad, void *stream);
+
+/* e4m3 quantization with one fp32 scale per block of 128 values, of the
+ * matrix Y = x or, with STCE_QUANT_TRANSPOSE, Y = x^T (x [R, C], dtype bf16,
+ * fp16 or fp32, row stride ld elements, 16-byte aligned rows not required).
+ * With Y of Q rows and L columns:
+ *   blocks:  128 consecutive columns of one row, or, with STCE_QUANT_TILE,
+ *            tiles of 128 rows x 128 columns (the last ones shorter);
+ *   scale  = fl32(largest |y| of the block / 448), 1 where that is 0;
+ *   code   = e4m3(clamp(fl32(y / scale), -448, 448)), nearest, ties to even.
+ * A block that holds a NaN or an infinity gets scale NaN and codes 0, so every
+ * product with it is NaN.  Writes codes [Q, round_up(L, 16)] (columns past L
+ * zero; row stride ld_codes, a multiple of 16; 16-byte aligned) and scales
+ * [ceil(L / 128)][Q or ceil(Q / 128)] fp32, the block index slowest: the
+ * operands of stce_fp8_block_matmul.  (The transposed forms are what a weight
+ * gradient, reduced over tokens, and a hidden gradient, reduced over the
+ * vocabulary, take.) */
+#define STCE_QUANT_TILE 1
+#define STCE_QUANT_TRANSPOSE 2
+stce_status stce_fp8_quantize_blocks(const void *x, int32_t dtype, int64_t R, int64_t C, int64_t ld, int32_t flags,
+                                     uint8_t *codes, int64_t ld_codes, float *scales, void *stream);
+
+/* Product of two e4m3 matrices with a scale for each block of 128 of the
+ * reduction:
+ *   out[m, n] (+)= sum_b sa[m, b] sb[n / b_rows, b] sum_{k in block b} a[m, k] b[n, k]
+ * a [M, K] and b [N, K] are e4m3 codes (K-major, row strides lda and ldb, all
+ * three multiples of 16; 16-byte aligned), sa one scale per row of a and block of 128 of k, sb per
+ * b_rows = 1 or 128 rows of b.  The scale of (row r, block b) is at
+ * scale[r * row_stride + b * block_stride].  Products of one block are summed
+ * in fp32 on the matrix cores, scaled and added to an fp32 sum (blocks in
+ * order; with few output tiles the reduction is cut into segments, summed in
+ * order from the workspace: the cut depends on the shapes only, so equal calls
+ * give equal bits).  out [M, N] bf16, fp16 or fp32 (rounded once), row stride
+ * ldo; with accumulate (fp32 only) the product is added to out.  K = 0 gives
+ * zeros; M or N = 0 does nothing. */
+typedef struct stce_block_matmul {
+  int64_t M, N, K;
+  const uint8_t *a;
+  int64_t lda;
+  const float *a_scale;
+  int64_t a_row_stride, a_block_stride;
+  const uint8_t *b;
+  int64_t ldb;
+  const float *b_scale;
+  int64_t b_row_stride, b_block_stride;
+  int32_t b_rows; /* rows of b per scale: 1 or 128 */
+  int32_t out_dtype;
+  void *out;
+  int64_t ldo;
+  int32_t accumulate;
+} stce_block_matmul;
+stce_status stce_fp8_block_matmul_workspace_bytes(const stce_block_matmul *p, size_t *bytes);
+stce_status stce_fp8_block_matmul(const stce_block_matmul *p, void *ws, size_t ws_bytes, void *stream);
 
 /* Human-readable name of a status code (static string). */
 const char *stce_status_string(stce_status status);

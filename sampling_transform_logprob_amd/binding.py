@@ -28,7 +28,8 @@ RECORD_BYTES = 32
 NTILE = 31
 NSP = 128
 STATE_BYTES_PER_ROW = RECORD_BYTES + 2 * (1 + NTILE) + 8 * NSP
-DT_BF16, DT_F32, DT_FP8 = 1, 2, 3
+DT_BF16, DT_F32, DT_FP8, DT_F16 = 1, 2, 3, 4
+VALUE_DTYPES = {torch.bfloat16: DT_BF16, torch.float16: DT_F16, torch.float32: DT_F32}
 # dtypes a weight of e4m3 codes may come in (the fp8 lane)
 FP8_WEIGHT_DTYPES = (torch.uint8, torch.float8_e4m3fn)
 
@@ -38,12 +39,17 @@ SYMBOLS = (
     "stce_decode_state", "stce_status_string", "stce_last_error", "stce_profile_attach", "stce_schedule",
     "stce_policy_loss", "stce_forward_with_side", "stce_fused_workspace_bytes", "stce_fused_policy_step",
     "stce_recompute_keys", "stce_forward_noalloc", "stce_noalloc_scratch_bytes", "stce_fp8_quantize_rows",
+    "stce_token_workspace_bytes", "stce_token_logprobs", "stce_token_logprobs_backward",
+    "stce_fp8_quantize_blocks", "stce_fp8_block_matmul_workspace_bytes", "stce_fp8_block_matmul",
 )
 KERNEL_KINDS = {1: "validate", 2: "projection", 3: "select", 4: "dlogits", 5: "grad_weight",
                 6: "grad_hidden", 7: "transpose", 8: "partials", 9: "policy_loss", 10: "dz_keys",
                 11: "split_sum", 12: "prescale", 13: "classify", 14: "sparse_grad_weight",
                 15: "sparse_grad_hidden", 16: "reproject", 17: "quantize", 18: "tile_lists",
-                19: "tile_recompute", 20: "listed_entries"}
+                19: "tile_recompute", 20: "listed_entries", 21: "token_logprobs", 22: "token_merge",
+                23: "token_grad", 24: "quantize_blocks", 25: "block_matmul"}
+QUANT_TILE, QUANT_TRANSPOSE = 1, 2
+FP8_BLOCK = 128
 PG_OBJECTIVES = {"cispo": 1, "clip": 2}
 
 
@@ -86,6 +92,31 @@ class SideOutputs(ctypes.Structure):
                 ("entropy_support", ctypes.c_void_p)]
 
 
+class TokenProblem(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int64), ("V", ctypes.c_int64), ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32),
+        ("logits", ctypes.c_void_p), ("ld", ctypes.c_int64), ("temperature", ctypes.c_void_p),
+        ("tokens", ctypes.c_void_p), ("K", ctypes.c_int32), ("top_n", ctypes.c_int32),
+        ("ignore_index", ctypes.c_int64),
+    ]
+
+
+class TokenOutputs(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("logprob", "lse", "entropy", "top_logprob", "top_id", "stats")]
+
+
+class BlockMatmul(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+        ("a", ctypes.c_void_p), ("lda", ctypes.c_int64), ("a_scale", ctypes.c_void_p),
+        ("a_row_stride", ctypes.c_int64), ("a_block_stride", ctypes.c_int64),
+        ("b", ctypes.c_void_p), ("ldb", ctypes.c_int64), ("b_scale", ctypes.c_void_p),
+        ("b_row_stride", ctypes.c_int64), ("b_block_stride", ctypes.c_int64),
+        ("b_rows", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("out", ctypes.c_void_p),
+        ("ldo", ctypes.c_int64), ("accumulate", ctypes.c_int32),
+    ]
+
+
 class StceError(RuntimeError):
     pass
 
@@ -124,6 +155,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "stce_fused_workspace_bytes": (ctypes.c_int, [P, ctypes.POINTER(sz), ctypes.POINTER(sz)]),
         "stce_fused_policy_step": (ctypes.c_int, [P, ctypes.POINTER(PgParams), vp, vp, vp, vp,
                                                   ctypes.POINTER(SideOutputs), vp, vp, i32, vp, vp, sz, vp]),
+        "stce_token_workspace_bytes": (ctypes.c_int, [ctypes.POINTER(TokenProblem), ctypes.POINTER(sz)]),
+        "stce_token_logprobs": (ctypes.c_int, [ctypes.POINTER(TokenProblem), ctypes.POINTER(TokenOutputs), vp, vp, sz,
+                                               vp]),
+        "stce_token_logprobs_backward": (ctypes.c_int, [ctypes.POINTER(TokenProblem), vp, vp, vp, vp, vp, i64, vp]),
+        "stce_fp8_quantize_blocks": (ctypes.c_int, [vp, i32, i64, i64, i64, i32, vp, i64, vp, vp]),
+        "stce_fp8_block_matmul_workspace_bytes": (ctypes.c_int, [ctypes.POINTER(BlockMatmul), ctypes.POINTER(sz)]),
+        "stce_fp8_block_matmul": (ctypes.c_int, [ctypes.POINTER(BlockMatmul), vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -246,7 +284,7 @@ def _raise_rows(status: torch.Tensor, what: str, tensors: dict) -> None:
     row, field = v >> 8, v & 0xFF
     name = FIELDS.get(field, f"field {field}")
     t = tensors.get(name)
-    val = "" if t is None else f"={t[row].item()!r}"
+    val = "" if t is None else f"={t[row].tolist()!r}"
     raise ValueError(f"{what}: invalid {name}[{row}]{val}")
 
 
@@ -591,3 +629,270 @@ class ScoreFunction(torch.autograd.Function):
         if gw is not None:
             gw = gw.to(weight.dtype)
         return (gh, gw) + (None,) * 8
+
+
+# ---------------------------------------------------------------------------
+# Operators on given arrays: token log probabilities, block-scaled fp8
+# quantization and product.  Their arrays may lie on any GPU: the call is made
+# on the arrays' device, on its current stream.
+# ---------------------------------------------------------------------------
+def _call(fn, dev, *args):
+    """fn(*args, stream) on the arrays' device, on its current stream."""
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream()))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream()))
+
+
+def _rows(name, x, dtypes):
+    """A 2-d GPU tensor of one of the dtypes with unit-stride rows (a copy
+    where the rows are not contiguous), and its row stride."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError(f"{name} must be a 2-d tensor")
+    if x.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {tuple(str(d) for d in dtypes)}, got {x.dtype}")
+    if x.device.type != "cuda":
+        raise ValueError(f"{name} must be on a GPU, got {x.device}")
+    R, C = x.shape
+    if (C > 1 and x.stride(1) != 1) or (R > 1 and x.stride(0) < C):
+        x = x.contiguous()
+    return x, (x.stride(0) if R > 1 and C else C)
+
+
+def _tokens(tokens, T, dev):
+    """([T, K] int64 or None, K, whether given as [T])."""
+    if tokens is None:
+        return None, 0, False
+    if not isinstance(tokens, torch.Tensor) or tokens.dtype != torch.int64:
+        raise TypeError("tokens must be an int64 tensor or None")
+    if tokens.device != dev:
+        raise ValueError(f"tokens is on {tokens.device}, expected {dev}")
+    if tokens.dim() not in (1, 2) or tokens.shape[0] != T:
+        raise ValueError(f"tokens must have shape [{T}] or [{T}, K], got {tuple(tokens.shape)}")
+    return tokens.contiguous(), (1 if tokens.dim() == 1 else tokens.shape[1]), tokens.dim() == 1
+
+
+def _token_problem(logits, tokens, temperature, top_n, ignore_index):
+    z, ld = _rows("logits", logits, VALUE_DTYPES)
+    T, V = z.shape
+    dev = z.device
+    tok, K, flat = _tokens(tokens, T, dev)
+    temp = _meta("temperature", temperature, T, torch.float32, dev)
+    prob = TokenProblem(T, V, VALUE_DTYPES[z.dtype], 0 if ignore_index is None else PROBLEM_IGNORE_INDEX,
+                        z.data_ptr(), max(ld, V), None if temp is None else temp.data_ptr(),
+                        None if tok is None else tok.data_ptr(), K, top_n,
+                        0 if ignore_index is None else int(ignore_index))
+    return prob, (z, tok, temp), flat
+
+
+def token_logprobs(logits, tokens=None, temperature=None, *, top_n: int = 0, ignore_index: Optional[int] = None,
+                   check: bool = True, workspace: Optional[torch.Tensor] = None):
+    """Log probabilities of given tokens under ``logits`` [T, V] (bf16, fp16 or
+    fp32; rows may be strided), scaled by a per-row ``temperature`` (fp32 [T]
+    or None).  ``tokens`` int64 [T] or [T, K].
+
+    Returns a dict: ``logprob`` (fp32, tokens' shape; absent without tokens),
+    ``lse`` and ``entropy`` (fp32 [T]), ``stats`` (fp32 [T, 4], for
+    ``token_logprobs_backward``) and, with ``top_n``, the ``top_n`` most likely
+    tokens of each row in order, lower id first among equal logits:
+    ``top_logprob`` (fp32 [T, top_n]) and ``top_id`` (int64; -1 past a row's
+    last token with a logit above -inf).  Masked tokens (-inf) score -inf;
+    ``ignore_index`` scores 0.  ``check=False`` skips the report of invalid
+    tokens and temperatures, which reads one number back from the GPU."""
+    prob, keep, flat = _token_problem(logits, tokens, temperature, top_n, ignore_index)
+    T, K = prob.T, prob.K
+    dev = logits.device
+    L = load()
+    nb = ctypes.c_size_t()
+    _check(L.stce_token_workspace_bytes(ctypes.byref(prob), ctypes.byref(nb)))
+    if workspace is None and nb.value:
+        workspace = torch.empty(nb.value, dtype=torch.uint8, device=dev)
+    out = dict(lse=torch.empty(T, dtype=torch.float32, device=dev),
+               entropy=torch.empty(T, dtype=torch.float32, device=dev),
+               stats=torch.empty(T, 4, dtype=torch.float32, device=dev))
+    if tokens is not None:
+        out["logprob"] = torch.empty(tokens.shape, dtype=torch.float32, device=dev)
+    if top_n:
+        out["top_logprob"] = torch.empty(T, top_n, dtype=torch.float32, device=dev)
+        out["top_id"] = torch.empty(T, top_n, dtype=torch.int64, device=dev)
+    status = torch.empty(1, dtype=torch.int64, device=dev) if check else None
+    o = TokenOutputs(*(out[k].data_ptr() if k in out else None
+                       for k in ("logprob", "lse", "entropy", "top_logprob", "top_id", "stats")))
+    _call(L.stce_token_logprobs, dev, ctypes.byref(prob), ctypes.byref(o), _ptr(status), _ptr(workspace),
+          0 if workspace is None else workspace.numel())
+    if check:
+        _raise_rows(status, "stce_token_logprobs", dict(temperature=keep[2], target=keep[1]))
+    return out
+
+
+def token_logprobs_backward(logits, tokens, stats, grad_logprob=None, grad_entropy=None, grad_lse=None, *,
+                            temperature=None, ignore_index: Optional[int] = None,
+                            grad_logits: Optional[torch.Tensor] = None):
+    """Gradient of ``sum(grad_logprob * logprob) + sum(grad_entropy * entropy)
+    + sum(grad_lse * lse)`` with respect to the logits, in their dtype; ``stats``
+    is the forward's.  ``grad_logits`` gives the result's place (strided rows
+    allowed; not overlapping the logits)."""
+    prob, keep, flat = _token_problem(logits, tokens, temperature, 0, ignore_index)
+    T, V, K = prob.T, prob.V, prob.K
+    dev = logits.device
+    if stats.shape != (T, 4) or stats.dtype != torch.float32 or stats.device != dev or not stats.is_contiguous():
+        raise ValueError("stats must be the contiguous fp32 [T, 4] tensor of the forward")
+    if grad_logprob is not None:
+        if tokens is None or grad_logprob.shape != tokens.shape:
+            raise ValueError("grad_logprob must have the tokens' shape")
+        if grad_logprob.dtype != torch.float32 or grad_logprob.device != dev:
+            raise ValueError("grad_logprob must be fp32 on the logits' device")
+        grad_logprob = grad_logprob.contiguous()
+    ge = _meta("grad_entropy", grad_entropy, T, torch.float32, dev)
+    gl = _meta("grad_lse", grad_lse, T, torch.float32, dev)
+    if grad_logits is None:
+        grad_logits = torch.empty(T, V, dtype=logits.dtype, device=dev)
+    elif (grad_logits.shape != (T, V) or grad_logits.dtype != logits.dtype or grad_logits.device != dev
+          or (V > 1 and grad_logits.stride(1) != 1) or (T > 1 and grad_logits.stride(0) < V)):
+        raise ValueError("grad_logits must have the logits' shape, dtype and device, with unit-stride rows")
+    ldg = max(grad_logits.stride(0), V) if T > 1 else max(V, 1)
+    _call(load().stce_token_logprobs_backward, dev, ctypes.byref(prob), _ptr(stats), _ptr(grad_logprob), _ptr(ge),
+          _ptr(gl), _ptr(grad_logits), ldg)
+    return grad_logits
+
+
+class TokenLogprobFunction(torch.autograd.Function):
+    """Autograd wrapper of ``token_logprobs``:
+
+    ``logprob, lse, entropy, top_logprob, top_id = TokenLogprobFunction.apply(logits, tokens, temperature,
+    ignore_index, top_n, check)`` (arguments after ``tokens`` optional; the
+    last two outputs None without ``top_n``).  Gradients flow from the first
+    three to the logits; the alternatives are values (score them as given
+    tokens to differentiate through them)."""
+
+    @staticmethod
+    def forward(ctx, logits, tokens, temperature=None, ignore_index=None, top_n=0, check=True):
+        out = token_logprobs(logits, tokens, temperature, top_n=top_n, ignore_index=ignore_index, check=check)
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(logits, tokens, out["stats"], temperature)
+        ctx.ignore_index = ignore_index
+        top = (out.get("top_logprob"), out.get("top_id"))
+        ctx.mark_non_differentiable(*(t for t in top if t is not None))
+        return (out.get("logprob"), out["lse"], out["entropy"]) + top
+
+    @staticmethod
+    def backward(ctx, g_logprob, g_lse, g_entropy, *_):
+        if g_logprob is None and g_lse is None and g_entropy is None:
+            return (None,) * 6
+        logits, tokens, stats, temperature = ctx.saved_tensors
+        g = token_logprobs_backward(logits, tokens, stats, g_logprob, g_entropy, g_lse, temperature=temperature,
+                                    ignore_index=ctx.ignore_index)
+        return (g,) + (None,) * 5
+
+
+def fp8_quantize_blocks(x: torch.Tensor, *, block: str = "row", transpose: bool = False):
+    """e4m3 codes and fp32 scales of ``x`` [R, C] (bf16, fp16 or fp32), one
+    scale per 128 values: of a row (``block="row"``) or of a 128 x 128 tile
+    (``block="tile"``); with ``transpose`` of the transposed matrix.  Returns
+    (codes float8_e4m3fn [Q, L rounded up to 16, zeros past L], scales [Q or
+    ceil(Q / 128), ceil(L / 128)]) with Q, L = R, C (transposed: C, R): the
+    operands of ``fp8_block_matmul``.  (The scales are a view with the block
+    index slowest in memory.)"""
+    if block not in ("row", "tile"):
+        raise ValueError("block must be 'row' or 'tile'")
+    x, ld = _rows("x", x, VALUE_DTYPES)
+    R, C = x.shape
+    Q, n = (C, R) if transpose else (R, C)
+    dev = x.device
+    kp = -(-n // 16) * 16
+    codes = torch.empty(Q, kp, dtype=torch.float8_e4m3fn, device=dev)
+    scales = torch.empty(-(-n // FP8_BLOCK), Q if block == "row" else -(-Q // FP8_BLOCK), dtype=torch.float32,
+                         device=dev)
+    flags = (QUANT_TILE if block == "tile" else 0) | (QUANT_TRANSPOSE if transpose else 0)
+    _call(load().stce_fp8_quantize_blocks, dev, _ptr(x), VALUE_DTYPES[x.dtype], R, C, max(ld, C), flags, _ptr(codes),
+          kp, _ptr(scales))
+    return codes, scales.t()
+
+
+def _fp8_operand(name, q, scale, tile_ok):
+    q, ld = _rows(name, q, FP8_WEIGHT_DTYPES)
+    R, K = q.shape
+    kb = -(-K // FP8_BLOCK)
+    if K % 16 or ld % 16 or q.data_ptr() % 16:
+        raise ValueError(f"{name} must have rows of a multiple of 16 codes, 16-byte aligned (fp8_quantize_blocks pads "
+                         f"them so), got {tuple(q.shape)} with row stride {ld}")
+    if not isinstance(scale, torch.Tensor) or scale.dtype != torch.float32 or scale.device != q.device:
+        raise TypeError(f"{name}_scale must be fp32 on {name}'s device")
+    tiles = (-(-R // FP8_BLOCK), kb)
+    if tuple(scale.shape) == (R, kb):
+        rows = 1
+    elif tile_ok and tuple(scale.shape) == tiles:
+        rows = FP8_BLOCK
+    else:
+        want = f"{(R, kb)}" + (f" or {tiles}" if tile_ok else "")
+        raise ValueError(f"{name}_scale must have shape {want}, got {tuple(scale.shape)}")
+    return q, ld, rows
+
+
+def fp8_block_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, *, out: Optional[torch.Tensor] = None,
+                     accumulate: bool = False, workspace: Optional[torch.Tensor] = None):
+    """``a @ b.T`` of e4m3 codes a [M, K] and b [N, K] (``float8_e4m3fn`` or
+    uint8, K a multiple of 16) with a scale per 128 of K: ``a_scale`` [M,
+    ceil(K / 128)], ``b_scale`` [N, ceil(K / 128)] or, per 128 x 128 tile,
+    [ceil(N / 128), ceil(K / 128)], fp32, any strides.  Returns ``out`` [M, N] in
+    ``out_dtype`` (bf16, fp16, fp32), rounded once from fp32 sums; with
+    ``accumulate`` the product is added to ``out`` (fp32)."""
+    a, lda, _ = _fp8_operand("a", a, a_scale, False)
+    b, ldb, b_rows = _fp8_operand("b", b, b_scale, True)
+    M, K = a.shape
+    N = b.shape[0]
+    dev = a.device
+    if b.shape[1] != K or b.device != dev:
+        raise ValueError(f"a and b must share K and the device, got {tuple(a.shape)}, {tuple(b.shape)}")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        if out_dtype not in VALUE_DTYPES:
+            raise TypeError(f"out_dtype must be bf16, fp16 or fp32, got {out_dtype}")
+        out = torch.empty(M, N, dtype=out_dtype, device=dev)
+    elif (out.shape != (M, N) or out.dtype not in VALUE_DTYPES or out.device != dev
+          or (N > 1 and out.stride(1) != 1) or (M > 1 and out.stride(0) < N)):
+        raise ValueError("out must be a bf16, fp16 or fp32 [M, N] tensor on the operands' device with unit-stride rows")
+    p = BlockMatmul(M, N, K, a.data_ptr(), lda, a_scale.data_ptr(), a_scale.stride(0),
+                    a_scale.stride(1), b.data_ptr(), ldb, b_scale.data_ptr(),
+                    b_scale.stride(0), b_scale.stride(1), b_rows, VALUE_DTYPES[out.dtype], out.data_ptr(),
+                    max(out.stride(0), N) if M > 1 else N, 1 if accumulate else 0)
+    L = load()
+    nb = ctypes.c_size_t()
+    _check(L.stce_fp8_block_matmul_workspace_bytes(ctypes.byref(p), ctypes.byref(nb)))
+    if workspace is None and nb.value:
+        workspace = torch.empty(nb.value, dtype=torch.uint8, device=dev)
+    _call(L.stce_fp8_block_matmul, dev, ctypes.byref(p), _ptr(workspace), 0 if workspace is None else workspace.numel())
+    return out
+
+
+class Fp8BlockLinearFunction(torch.autograd.Function):
+    """``Fp8BlockLinearFunction.apply(x, weight)``: the linear layer (or head)
+    ``x @ weight.T`` of bf16, fp16 or fp32 x [T, H] and weight [V, H] on e4m3
+    operands with block scales (x per row and 128 values, the weight per 128 x
+    128 tile), in x's dtype.  The gradients pass the quantizations straight
+    through and are such products themselves: the incoming gradient and the
+    weight's transpose for dx, both transposed to reduce over the rows for
+    dweight, each quantized along its reduction; dweight in the weight's dtype."""
+
+    @staticmethod
+    def forward(ctx, x, weight):
+        xq, xs = fp8_quantize_blocks(x)
+        wq, ws = fp8_quantize_blocks(weight, block="tile")
+        ctx.save_for_backward(x, weight)
+        return fp8_block_matmul(xq, xs, wq, ws, out_dtype=x.dtype)
+
+    @staticmethod
+    def backward(ctx, g):
+        x, weight = ctx.saved_tensors
+        gx = gw = None
+        if ctx.needs_input_grad[0]:
+            gq, gs = fp8_quantize_blocks(g)
+            wq, ws = fp8_quantize_blocks(weight, block="tile", transpose=True)
+            gx = fp8_block_matmul(gq, gs, wq, ws, out_dtype=x.dtype)
+        if ctx.needs_input_grad[1]:
+            gq, gs = fp8_quantize_blocks(g, transpose=True)
+            xq, xs = fp8_quantize_blocks(x, transpose=True)
+            gw = fp8_block_matmul(gq, gs, xq, xs, out_dtype=weight.dtype)
+        return gx, gw

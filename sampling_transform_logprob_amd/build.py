@@ -8,7 +8,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libstce.so")
-SOURCES = ["kernels.hip", "select.hip", "sparse.hip", "api.hip"]
+SOURCES = ["kernels.hip", "select.hip", "sparse.hip", "api.hip", "token_logprob.hip", "block_fp8.hip",
+           "ops_api.hip"]
 
 FLAGS = [
     "-O3", "--offload-arch=gfx950", "-std=c++17", "-fPIC", "-shared",

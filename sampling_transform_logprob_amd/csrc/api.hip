@@ -9,6 +9,7 @@
 #include <unordered_map>
 
 #include "../../include/stce.h"
+#include "api_internal.hpp"
 #include "kernels.hpp"
 
 using namespace stce;
@@ -26,6 +27,10 @@ thread_local char g_err[512] = "";
 thread_local stce_profile* g_prof = nullptr;
 thread_local int g_prof_open = -1;
 
+}  // namespace
+
+namespace stce {
+
 stce_status fail(stce_status s, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -37,6 +42,10 @@ stce_status fail(stce_status s, const char* fmt, ...) {
 stce_status hip_fail(hipError_t e, const char* what) {
   return fail(STCE_E_HIP, "%s: %s", what, hipGetErrorString(e));
 }
+
+}  // namespace stce
+
+namespace {
 
 constexpr int kComputeUnits = 256;       // MI355X (gfx950): 8 XCDs of 32
 // Bytes the default chunking lets the two chunk buffers' fp32 keys take.

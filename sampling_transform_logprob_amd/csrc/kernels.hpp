@@ -12,7 +12,8 @@ enum : int {
   KIND_GRAD_HIDDEN = 6, KIND_TRANSPOSE = 7, KIND_PARTIALS = 8, KIND_POLICY_LOSS = 9, KIND_DZ_KEYS = 10,
   KIND_SPLIT_SUM = 11, KIND_PRESCALE = 12, KIND_CLASSIFY = 13, KIND_SPARSE_DW = 14, KIND_SPARSE_DH = 15,
   KIND_REPROJECT = 16, KIND_QUANTIZE = 17, KIND_TILE_LISTS = 18, KIND_TILE_RECOMPUTE = 19,
-  KIND_LISTED_ENTRIES = 20
+  KIND_LISTED_ENTRIES = 20, KIND_TOKEN_LOGPROBS = 21, KIND_TOKEN_MERGE = 22, KIND_TOKEN_GRAD = 23,
+  KIND_QUANTIZE_BLOCKS = 24, KIND_BLOCK_MATMUL = 25
 };
 
 // Launch-timing hook (no-op unless a profile is attached to this thread).

@@ -1,0 +1,249 @@
+"""Host side of the operators on given arrays, and pins of their fp64 oracle:
+argument refusals before anything is launched (no device call is made here),
+struct layouts against the C compiler's, and the oracle against torch's
+log_softmax, fp64 autograd, finite differences and float8 conversion."""
+import ctypes
+import os
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import head_ops_oracle as ref
+from sampling_transform_logprob_amd import binding
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(binding.LIB_PATH):
+        pytest.skip("libstce.so not built")
+    return binding.load()
+
+
+@pytest.mark.parametrize("name,struct", [("stce_token_problem", binding.TokenProblem),
+                                         ("stce_token_outputs", binding.TokenOutputs),
+                                         ("stce_block_matmul", binding.BlockMatmul)])
+def test_struct_layouts_match_the_header(tmp_path, name, struct):
+    fields = [f for f, _ in struct._fields_]
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "stce.h"\nint main(void) {\n'
+                   f'  printf("%zu\\n", sizeof({name}));\n'
+                   + "".join(f'  printf("%zu\\n", offsetof({name}, {f}));\n' for f in fields) + "  return 0;\n}\n")
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    out = [int(x) for x in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()]
+    assert out[0] == ctypes.sizeof(struct)
+    assert out[1:] == [getattr(struct, f).offset for f in fields]
+
+
+FAKE = 4096  # an aligned address that is never read: the calls below are refused
+
+
+def _token(**kw):
+    d = dict(T=4, V=100, dtype=binding.DT_BF16, logits=FAKE, ld=100, tokens=FAKE, K=1)
+    d.update(kw)
+    p = binding.TokenProblem()
+    for k, v in d.items():
+        setattr(p, k, v)
+    return p
+
+
+@pytest.mark.parametrize("kw,msg", [
+    (dict(dtype=binding.DT_FP8), b"unsupported logits dtype"), (dict(dtype=0), b"unsupported logits dtype"),
+    (dict(T=-1), b"T=-1"), (dict(T=(1 << 24) + 1), b"T="), (dict(V=0, ld=0), b"V=0"), (dict(V=2**31, ld=2**31), b"V="),
+    (dict(ld=99), b"ld=99"), (dict(ld=2**61), b"ld="), (dict(K=-1), b"K=-1"), (dict(K=1025), b"K=1025"),
+    (dict(top_n=129), b"top_n=129"), (dict(top_n=-1), b"top_n=-1"), (dict(flags=2), b"flags=2"),
+    (dict(flags=1, ignore_index=99), b"ignore_index=99"), (dict(logits=None), b"required"),
+    (dict(tokens=None), b"required"), (dict(logits=FAKE + 1), b"aligned"), (dict(tokens=FAKE + 4), b"aligned"),
+    (dict(temperature=FAKE + 2), b"aligned"),
+])
+def test_token_problem_refusals(lib, kw, msg):
+    p = _token(**kw)
+    out = binding.TokenOutputs(FAKE)
+    st = lib.stce_token_logprobs(ctypes.byref(p), ctypes.byref(out), None, ctypes.c_void_p(FAKE), 1 << 40, None)
+    assert st in (1, 2) and msg in lib.stce_last_error(), lib.stce_last_error()
+    if "top_n" not in kw:
+        st = lib.stce_token_logprobs_backward(ctypes.byref(p), ctypes.c_void_p(FAKE), ctypes.c_void_p(FAKE), None, None,
+                                              ctypes.c_void_p(1 << 50), 2**30, None)
+        assert st in (1, 2) and msg in lib.stce_last_error(), lib.stce_last_error()
+
+
+def test_token_output_refusals(lib):
+    p = _token()
+    ws = (ctypes.c_void_p(FAKE), 1 << 40, None)
+    assert lib.stce_token_logprobs(ctypes.byref(p), None, None, *ws) == 1
+    assert lib.stce_token_logprobs(ctypes.byref(p), ctypes.byref(binding.TokenOutputs(None, None, None, None, None,
+                                                                                      FAKE + 4)), None, *ws) == 1
+    assert b"aligned" in lib.stce_last_error()
+    back = lambda *a: lib.stce_token_logprobs_backward(ctypes.byref(p), *a, None)  # noqa: E731
+    v = ctypes.c_void_p
+    assert back(None, v(FAKE), None, None, v(1 << 50), 100) == 1 and b"stats" in lib.stce_last_error()
+    assert back(v(FAKE), v(FAKE), None, None, None, 100) == 1 and b"grad_logits" in lib.stce_last_error()
+    assert back(v(FAKE), v(FAKE), None, None, v(1 << 50), 99) == 1 and b"ld_grad=99" in lib.stce_last_error()
+    # the last byte of the logits (4 rows of 100 bf16) is inside the gradient
+    assert back(v(FAKE), v(FAKE), None, None, v(FAKE + 798), 100) == 1 and b"overlaps" in lib.stce_last_error()
+    assert lib.stce_token_workspace_bytes(ctypes.byref(p), None) == 1
+
+
+def test_small_token_workspace_is_refused(lib):
+    p = _token(T=1, V=200000, ld=200000, top_n=20)
+    n = ctypes.c_size_t()
+    assert lib.stce_token_workspace_bytes(ctypes.byref(p), ctypes.byref(n)) == 0
+    if n.value:
+        out = binding.TokenOutputs(FAKE)
+        for ws, size in ((None, n.value), (FAKE, n.value - 1), (FAKE + 16, n.value)):
+            st = lib.stce_token_logprobs(ctypes.byref(p), ctypes.byref(out), None, ctypes.c_void_p(ws), size, None)
+            assert st in (1, 3) and b"workspace" in lib.stce_last_error()
+
+
+def test_quantize_refusals(lib):
+    def call(x=FAKE, dtype=1, R=4, C=32, ld=32, flags=0, codes=FAKE, ldc=32, scales=FAKE):
+        v = ctypes.c_void_p
+        return lib.stce_fp8_quantize_blocks(v(x), dtype, R, C, ld, flags, v(codes), ldc, v(scales), None)
+    for kw, msg in [(dict(dtype=3), b"unsupported input dtype"), (dict(flags=4), b"flags=4"), (dict(R=-1), b"R=-1"),
+                    (dict(C=-1, ld=0), b"C=-1"), (dict(R=2**28 + 1), b"R="), (dict(C=2**22 + 1, ld=2**23), b"C="),
+                    (dict(R=2**22 + 1, flags=2), b"R="), (dict(ld=31), b"ld=31"), (dict(ldc=16), b"ld_codes=16"),
+                    (dict(ldc=40), b"ld_codes=40"), (dict(C=33, ld=33), b"ld_codes=32"), (dict(x=None), b"required"),
+                    (dict(codes=None), b"required"), (dict(scales=None), b"required"), (dict(x=FAKE + 1), b"aligned"),
+                    (dict(codes=FAKE + 8), b"aligned"), (dict(scales=FAKE + 2), b"aligned")]:
+        assert call(**kw) in (1, 2) and msg in lib.stce_last_error(), (kw, lib.stce_last_error())
+    assert call(x=None, R=0) == 0 and call(x=None, C=0, ld=0) == 0     # nothing to do
+
+
+def _matmul(**kw):
+    d = dict(M=4, N=8, K=64, a=FAKE, lda=64, a_scale=FAKE, a_row_stride=1, a_block_stride=4, b=FAKE, ldb=64,
+             b_scale=FAKE, b_row_stride=1, b_block_stride=8, b_rows=1, out_dtype=2, out=FAKE, ldo=8)
+    d.update(kw)
+    p = binding.BlockMatmul()
+    for k, v in d.items():
+        setattr(p, k, v)
+    return p
+
+
+@pytest.mark.parametrize("kw,msg", [
+    (dict(out_dtype=3), b"unsupported output dtype"), (dict(M=-1), b"M=-1"), (dict(N=2**31), b"N="),
+    (dict(K=2**22 + 16, lda=2**23, ldb=2**23), b"K="), (dict(K=24), b"multiples of 16"),
+    (dict(lda=72), b"multiples of 16"), (dict(ldb=48), b"ldb=48"), (dict(lda=2**22 + 16), b"at most 2^22"),
+    (dict(ldo=7), b"ldo=7"), (dict(b_rows=64), b"b_rows=64"), (dict(a_row_stride=-1), b"strides"),
+    (dict(accumulate=1, out_dtype=1), b"accumulate"), (dict(a=None), b"required"), (dict(b_scale=None), b"required"),
+    (dict(out=None), b"required"), (dict(a=FAKE + 8), b"aligned"), (dict(b_scale=FAKE + 1), b"aligned"),
+    (dict(out=FAKE + 2), b"aligned"),
+])
+def test_block_matmul_refusals(lib, kw, msg):
+    p = _matmul(**kw)
+    st = lib.stce_fp8_block_matmul(ctypes.byref(p), ctypes.c_void_p(FAKE), 1 << 40, None)
+    assert st in (1, 2) and msg in lib.stce_last_error(), lib.stce_last_error()
+
+
+def test_empty_products_do_nothing(lib):
+    for kw in (dict(M=0, out=None, a=None), dict(N=0, ldo=0, out=None, b=None)):
+        assert lib.stce_fp8_block_matmul(ctypes.byref(_matmul(**kw)), None, 0, None) == 0
+
+
+def test_binding_refusals():
+    z, t = torch.zeros(3, 8), torch.zeros(3, dtype=torch.int64)
+    with pytest.raises(ValueError, match="on a GPU"):
+        binding.token_logprobs(z, t)
+    with pytest.raises(TypeError, match="logits"):
+        binding.token_logprobs(z.double(), t)
+    with pytest.raises(ValueError, match="2-d"):
+        binding.token_logprobs(z[0], t)
+    with pytest.raises(ValueError, match="block must be"):
+        binding.fp8_quantize_blocks(z, block="column")
+    with pytest.raises(TypeError, match="x must be"):
+        binding.fp8_quantize_blocks(z.to(torch.int32))
+    with pytest.raises(TypeError, match="a must be"):
+        binding.fp8_block_matmul(z, z, z, z)
+
+
+# ---------------------------------------------------------------------------
+# the oracle against independent definitions
+# ---------------------------------------------------------------------------
+def _example(rng, T=6, V=23):
+    z = rng.standard_normal((T, V)) * 3
+    z[1, ::2] = -np.inf
+    z[2] = -np.inf
+    z[3, 4:9] = z[3, 4]                     # ties
+    tok = rng.integers(0, V, (T, 4))
+    tok[:, 3] = tok[:, 0]
+    tok[4, 1] = -100
+    temp = rng.uniform(0.5, 1.5, T)
+    return z, tok, temp
+
+
+def test_oracle_logprobs_are_torchs(rng):
+    z, tok, temp = _example(rng)
+    r = ref.token_logprobs(z, tok, temp, top_n=30, ignore_index=-100)
+    live = [0, 1, 3, 4, 5]
+    lp = torch.log_softmax(torch.tensor(z[live]) / torch.tensor(temp[live])[:, None], 1)
+    want = lp.gather(1, torch.tensor(np.maximum(tok[live], 0))).numpy()
+    want[3, 1] = 0.0
+    assert np.allclose(r["logprob"][live], want, rtol=0, atol=1e-13)
+    p = lp.exp().numpy()
+    ent = -(p * np.where(p > 0, lp.numpy(), 0)).sum(1)
+    assert np.allclose(r["entropy"][live], ent, atol=1e-13)
+    assert np.all(r["logprob"][2] == -np.inf) and r["lse"][2] == -np.inf and r["entropy"][2] == 0
+    assert np.all(r["top_id"][2] == -1)
+    ids = r["top_id"][3][:23]
+    assert sorted(ids) == list(range(23))
+    vals = z[3, ids]
+    assert all((a > b) or (a == b and i < j) for a, b, i, j in zip(vals, vals[1:], ids, ids[1:]))
+    assert np.all(r["top_id"][3][23:] == -1) and (r["top_id"][1] >= 0).sum() == 11
+
+
+def test_oracle_gradient_is_autograds_and_the_difference_quotients(rng):
+    z, tok, temp = _example(rng)
+    z[1, ::2] = -2.0                        # differences need finite logits
+    live = [0, 1, 3, 4, 5]
+    z, tok, temp = z[live], tok[live], temp[live]
+    g, ge, gl = rng.standard_normal(tok.shape), rng.standard_normal(5), rng.standard_normal(5)
+
+    def loss(zz):
+        r = ref.token_logprobs(zz, tok, temp, ignore_index=-100)
+        return (g * r["logprob"]).sum() + (ge * r["entropy"]).sum() + (gl * r["lse"]).sum()
+    d = ref.token_logprobs_backward(z, tok, g, ge, gl, temp, -100)
+    zt = torch.tensor(z, requires_grad=True)
+    lp = torch.log_softmax(zt / torch.tensor(temp)[:, None], 1)
+    mask = torch.tensor(tok != -100)
+    obj = ((torch.tensor(g) * mask) * lp.gather(1, torch.tensor(np.maximum(tok, 0)))).sum()
+    obj = obj - (torch.tensor(ge) * (lp.exp() * lp).sum(1)).sum()
+    obj = obj + (torch.tensor(gl) * torch.logsumexp(zt / torch.tensor(temp)[:, None], 1)).sum()
+    obj.backward()
+    assert np.allclose(d, zt.grad.numpy(), atol=1e-12)
+    eps = 1e-6
+    for t, j in [(0, 0), (0, int(tok[0, 0])), (2, 5), (3, int(tok[3, 2])), (4, 22)]:
+        up, dn = z.copy(), z.copy()
+        up[t, j] += eps
+        dn[t, j] -= eps
+        assert abs((loss(up) - loss(dn)) / (2 * eps) - d[t, j]) < 1e-8
+
+
+def test_oracle_masked_tokens_pass_no_gradient():
+    z = np.array([[0.0, -np.inf, 1.0]])
+    d = ref.token_logprobs_backward(z, np.array([[1]]), np.array([[1.0]]))
+    assert np.all(d == 0)
+
+
+def test_oracle_codes_are_torchs(rng):
+    x = np.concatenate([rng.uniform(-448, 448, 4000), rng.uniform(-0.05, 0.05, 4000),
+                        ref.e4m3_values()[:127], (ref.e4m3_values()[:126] + ref.e4m3_values()[1:127]) / 2, [-0.0]])
+    x = x.astype(np.float32)
+    got = torch.tensor(x).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    assert np.array_equal(ref.e4m3_nearest(x), got)
+    vals = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).float().numpy()
+    assert np.array_equal(np.nan_to_num(vals, nan=7.5), np.nan_to_num(ref.e4m3_values(), nan=7.5))
+
+
+def test_oracle_quantization_restores_the_matrix(rng):
+    x = rng.standard_normal((150, 300)).astype(np.float32)
+    x[3, 128:256] = 0
+    for block, tr in (("row", False), ("row", True), ("tile", False), ("tile", True)):
+        q, s = ref.quantize_blocks(x, block, tr)
+        y = x.T if tr else x
+        d = ref.dequantize(q, s, 1 if block == "row" else 128)[:, :y.shape[1]]
+        amax = np.abs(y).max()
+        # half a step of e4m3: 2^-4 of the value, or 2^-10 of the scale below the normal range
+        assert np.all(np.abs(d - y) <= np.maximum(np.abs(y) * 2.0 ** -4, amax / 448 * 2.0 ** -10) * (1 + 1e-6))
