@@ -1,7 +1,7 @@
 // e4m3 quantization with a scale per block of 128, and the product of two
 // such matrices.
+#include "block_gemm.hpp"
 #include "epilogues.hpp"
-#include "gemm.hpp"
 #include "ops.hpp"
 
 namespace stce {
@@ -80,81 +80,296 @@ hipError_t run_quantize(const X* x, int64_t R, int64_t C, int64_t ld, int flags,
   return hipGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// product
+// ---------------------------------------------------------------------------
+// Four neighbouring outputs of one row, n of which exist, rounded to O (added
+// to what is there with add).
 template <class O>
-__device__ inline O to_out(float v) {
-  return (O)v;
-}
-
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
-// Eight e4m3 codes as fp16 (exact: e4m3's smallest value 2^-9 is normal there).
-__device__ inline f16x8 codes_f16(u32x2 c) {
-  u32x4 r;
+struct __attribute__((packed, aligned(sizeof(O)))) Out4 {
+  O v[4];
+};
+template <class O>
+__device__ inline void store4(O* dst, f32x4 v, int n, bool add) {
+  if (n >= 4) {
+    Out4<O> o;
+    if (add) {
+      o = *(const Out4<O>*)dst;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    r[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[i], 1.0f, false));
-    r[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[i], 1.0f, true));
+      for (int r = 0; r < 4; ++r) v[r] += (float)o.v[r];
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o.v[r] = (O)v[r];
+    *(Out4<O>*)dst = o;
+  } else {
+#pragma unroll
+    for (int r = 0; r < 3; ++r)
+      if (r < n) dst[r] = (O)(add ? (float)dst[r] + v[r] : v[r]);
   }
-  return __builtin_bit_cast(f16x8, r);
 }
 
-// One wave per 16 x 16 block of the output, operands straight from memory.
-// The fp8 matrix instructions align the eight products of each group of
-// consecutive k to the largest and drop what lies more than 13 binary places
-// below it (measured: 1.5e-5 of a 128-term sum of normal values, relative);
-// the fp16 ones sum the same products, exact after the conversion, to 9e-9.
-template <class O>
-__global__ __launch_bounds__(64) void block_matmul_simple_kernel(stce_block_matmul p) {
-  const int lane = threadIdx.x, row = lane & 15, quad = lane >> 4;
-  const int64_t m0 = (int64_t)blockIdx.y * 16, n0 = (int64_t)blockIdx.x * 16;
-  const int64_t m = m0 + row, n = n0 + row;
-  const int64_t mr = m < p.M ? m : p.M - 1, nr = n < p.N ? n : p.N - 1;
-  const uint8_t* a = p.a + mr * p.lda;
-  const uint8_t* b = p.b + nr * p.ldb;
-  f32x4 sum{};
-  for (int64_t k0 = 0, kb = 0; k0 < p.K; k0 += QB, ++kb) {
-    u32x4 va[2] = {}, vb[2] = {};
+struct BlockOut {
+  void* out;
+  int64_t ldo;
+  int64_t split;  // elements between the partial results of two segments (0: one segment)
+  int add;
+};
+
+// 256 rows of b by 64 NJ rows of a per workgroup; segment g of the reduction
+// (blocks [g per, (g + 1) per)) goes to its own partial output.
+template <int NJ, bool ROWB, class F, class O>
+__global__ __launch_bounds__(512, 1) void block_tile_kernel(BlockOps p, BlockOut o, TileMap map, int per) {
+  using Main = BlockMain<NJ, ROWB, F>;
+  const int tiles = map.tiles_m * map.tiles_n;
+  const int g = blockIdx.x / tiles;
+  int tn, tm;
+  map.get(blockIdx.x - g * tiles, tn, tm);
+  const int n0 = tn * Main::TN, m0 = tm * Main::TM;
+  const int nkb = (p.K + QB - 1) / QB;
+  typename Main::Acc acc;
+  Main::run(p, acc, n0, m0, g * per, min((g + 1) * per, nkb));
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  O* const out = (O*)o.out + g * o.split;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int m = m0 + (w & 3) * 16 * NJ + j * 16 + (lane & 15);
+    if (m >= p.M) continue;
+    O* const row = out + (int64_t)m * o.ldo;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int n = n0 + (w >> 2) * 128 + i * 16 + (lane >> 4) * 4;
+      store4(row + n, acc[i][j], p.N - n, o.add);
+    }
+  }
+}
+
+// Few rows of a (at most 16 TG): bound by b's bytes, which go from memory to
+// registers without LDS (no wave shares them).  A workgroup of four waves
+// forms 16 RG rows of b by all rows of a; the waves take the reduction's blocks
+// in turn (neighbouring 128-byte pieces of the same rows) and their sums are
+// added in wave order.  Every product is exact: fp16 matrix instructions, whose
+// rate does not matter here.
+template <int RG, int TG, bool ROWB, class O>
+__global__ __launch_bounds__(256) void block_skinny_kernel(BlockOps p, BlockOut o, int per) {
+  __shared__ f32x4 sums[4][RG * TG][64];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row = lane & 15, q = lane >> 4;
+  const int n0 = blockIdx.x * 16 * RG, g = blockIdx.y;
+  const int nkb = (p.K + QB - 1) / QB;
+  const int kb0 = g * per, kb1 = min(kb0 + per, nkb);
+  const uint8_t* pb[RG];
+  const uint8_t* pa[TG];
+  const float* psa[TG];
+#pragma unroll
+  for (int i = 0; i < RG; ++i) pb[i] = p.b + (int64_t)min(n0 + i * 16 + row, p.N - 1) * p.ldb + q * 16;
+#pragma unroll
+  for (int j = 0; j < TG; ++j) {
+    const int m = min(j * 16 + row, p.M - 1);
+    pa[j] = p.a + (int64_t)m * p.lda + q * 16;
+    psa[j] = p.sa + (int64_t)m * p.sa_row;
+  }
+  struct Tile {
+    u32x4 b[RG][2], a[TG][2];
+    float sa[TG], sb[ROWB ? RG * 4 : 1];
+  };
+  auto load = [&](Tile& t, int kb) __attribute__((always_inline)) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int64_t k = k0 + quad * 32 + h * 16;
-      if (k < p.K) {
-        va[h] = *(const u32x4*)(a + k);
-        vb[h] = *(const u32x4*)(b + k);
+      const int k = kb * QB + h * 64;
+      const bool in = k + q * 16 < p.K;
+#pragma unroll
+      for (int i = 0; i < RG; ++i) t.b[i][h] = in ? *(const u32x4*)(pb[i] + k) : u32x4{};
+#pragma unroll
+      for (int j = 0; j < TG; ++j) t.a[j][h] = in ? *(const u32x4*)(pa[j] + k) : u32x4{};
+    }
+#pragma unroll
+    for (int j = 0; j < TG; ++j) t.sa[j] = psa[j][kb * p.sa_blk];
+    if constexpr (ROWB) {
+#pragma unroll
+      for (int i = 0; i < RG; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          t.sb[i * 4 + r] = p.sb[(int64_t)min(n0 + i * 16 + q * 4 + r, p.N - 1) * p.sb_row + kb * p.sb_blk];
+    } else {
+      t.sb[0] = p.sb[(int64_t)(n0 / QB) * p.sb_row + kb * p.sb_blk];  // (16 RG rows lie in one tile)
+    }
+  };
+  f32x4 acc[RG][TG];
+#pragma unroll
+  for (int i = 0; i < RG; ++i)
+#pragma unroll
+    for (int j = 0; j < TG; ++j) acc[i][j] = f32x4{};
+  auto mul = [&](const Tile& t) __attribute__((always_inline)) {
+    FragF16 fa[TG];
+#pragma unroll
+    for (int j = 0; j < TG; ++j) fa[j] = FragF16(raw_frag(t.a[j][0], t.a[j][1]));
+#pragma unroll
+    for (int i = 0; i < RG; ++i) {
+      const FragF16 fb(raw_frag(t.b[i][0], t.b[i][1]));
+#pragma unroll
+      for (int j = 0; j < TG; ++j) {
+        const f32x4 part = block_mfma(fb, fa[j]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[i][j][r] = __builtin_fmaf(part[r], t.sa[j] * t.sb[ROWB ? i * 4 + r : 0], acc[i][j][r]);
       }
     }
-    f32x4 part{};
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        part = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16(u32x2{vb[h][2 * e], vb[h][2 * e + 1]}),
-                                                      codes_f16(u32x2{va[h][2 * e], va[h][2 * e + 1]}), part, 0, 0, 0);
-    const float sa = p.a_scale[mr * p.a_row_stride + kb * p.a_block_stride];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      int64_t nn = n0 + quad * 4 + r;
-      nn = nn < p.N ? nn : p.N - 1;
-      const float sb = p.b_scale[(p.b_rows == QB ? nn / QB : nn) * p.b_row_stride + kb * p.b_block_stride];
-      sum[r] = __builtin_fmaf(part[r], sa * sb, sum[r]);
+  };
+  Tile t[2];
+  int kb = kb0 + w;
+  if (kb < kb1) load(t[0], kb);
+  for (; kb < kb1; kb += 8) {
+    if (kb + 4 < kb1) load(t[1], kb + 4);
+    mul(t[0]);
+    if (kb + 4 < kb1) {
+      if (kb + 8 < kb1) load(t[0], kb + 8);
+      mul(t[1]);
     }
   }
-  if (m >= p.M) return;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int64_t nn = n0 + quad * 4 + r;
-    if (nn >= p.N) continue;
-    O* o = (O*)p.out + m * p.ldo + nn;
-    *o = to_out<O>(p.accumulate ? (float)*o + sum[r] : sum[r]);
+  for (int i = 0; i < RG; ++i)
+#pragma unroll
+    for (int j = 0; j < TG; ++j) sums[w][i * TG + j][lane] = acc[i][j];
+  __syncthreads();
+  O* const out = (O*)o.out + g * o.split;
+  for (int s = w; s < RG * TG; s += 4) {
+    f32x4 v = sums[0][s][lane];
+#pragma unroll
+    for (int x = 1; x < 4; ++x) v += sums[x][s][lane];
+    const int m = (s % TG) * 16 + row, n = n0 + (s / TG) * 16 + q * 4;
+    if (m < p.M && n < p.N) store4(out + (int64_t)m * o.ldo + n, v, p.N - n, o.add);
+  }
+}
+
+// out (+)= the segments' partial results [S][M][N], added in order.
+template <class O>
+__global__ __launch_bounds__(256) void block_sum_kernel(const float* part, int S, int64_t M, int64_t N, O* out,
+                                                        int64_t ldo, int add) {
+  const int64_t total = M * N;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
+    float v = part[e];
+    for (int s = 1; s < S; ++s) v += part[s * total + e];
+    O* dst = out + e / N * ldo + e % N;
+    *dst = (O)(add ? (float)*dst + v : v);
   }
 }
 
 template <class O>
-hipError_t run_matmul(const stce_block_matmul& p, hipStream_t s) {
+__global__ __launch_bounds__(256) void block_zero_kernel(int64_t M, int64_t N, O* out, int64_t ldo) {
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < M * N; e += (int64_t)gridDim.x * 256)
+    out[e / N * ldo + e % N] = (O)0.0f;
+}
+
+// How a product is cut: rows of a up to 64 take the skinny kernel.  Segments of
+// the reduction fill the chip when there are few output tiles.
+struct BlockPlan {
+  bool skinny;
+  int rg, tg, nj;      // skinny: 16-row groups of b and of a; tiled: NJ
+  int64_t tiles_n, tiles_m;
+  int S, per;          // segments, blocks per segment
+};
+
+BlockPlan plan_product(const stce_block_matmul& p) {
+  BlockPlan b{};
+  const int64_t nkb = ceil_div(p.K, QB);
+  int64_t wgs, want, least;  // workgroups of one segment, wanted in all, blocks a segment has at least
+  b.skinny = p.M <= 64;
+  if (b.skinny) {
+    b.rg = ceil_div(p.N, 64) >= 384 ? 4 : 1;
+    b.tg = p.M <= 16 ? 1 : p.M <= 32 ? 2 : 4;
+    b.tiles_n = ceil_div(p.N, 16 * b.rg);
+    wgs = b.tiles_n;
+    want = 512;
+    least = 4;
+  } else {
+    b.nj = p.M > 128 && p.out_dtype != STCE_DT_F32 && p.b_rows == QB ? 4 : 2;
+    b.tiles_n = ceil_div(p.N, 256);
+    b.tiles_m = ceil_div(p.M, 64 * b.nj);
+    wgs = b.tiles_n * b.tiles_m;
+    want = 256;
+    least = 4;
+  }
+  int64_t S = wgs >= want ? 1 : want / wgs;
+  if (S > ceil_div(nkb, least)) S = ceil_div(nkb, least);
+  if (S < 1) S = 1;
+  b.per = (int)ceil_div(nkb, S);
+  b.S = nkb ? (int)ceil_div(nkb, b.per) : 1;
+  return b;
+}
+
+template <bool ROWB, class O>
+void launch_skinny(const BlockPlan& b, const BlockOps& p, const BlockOut& o, hipStream_t s) {
+  const dim3 grid((unsigned)b.tiles_n, (unsigned)b.S);
+#define STCE_SKINNY(RG, TG) \
+  if (b.rg == RG && b.tg == TG) \
+  hipLaunchKernelGGL((block_skinny_kernel<RG, TG, ROWB, O>), grid, dim3(256), 0, s, p, o, b.per)
+  STCE_SKINNY(1, 1);
+  STCE_SKINNY(1, 2);
+  STCE_SKINNY(1, 4);
+  STCE_SKINNY(4, 1);
+  STCE_SKINNY(4, 2);
+  STCE_SKINNY(4, 4);
+#undef STCE_SKINNY
+}
+
+template <int NJ, bool ROWB, class F, class O>
+void launch_tiles(const BlockPlan& b, const BlockOps& p, const BlockOut& o, hipStream_t s) {
+  const TileMap map{(int)b.tiles_n, (int)b.tiles_m, 4};
+  hipLaunchKernelGGL((block_tile_kernel<NJ, ROWB, F, O>), dim3((unsigned)(b.tiles_n * b.tiles_m * b.S)), dim3(512), 0,
+                     s, p, o, map, b.per);
+}
+
+// A 16-bit output is rounded far above what the fp8 matrix instructions drop
+// (they align the eight products of a group of consecutive k to the largest
+// and keep 13 binary places below it: 1.5e-5 of a 128-term sum of normal
+// values); an fp32 output takes the fp16 ones on converted codes, exact
+// products summed to 9e-9, at half the rate.
+template <bool ROWB, class O, bool EXACT>
+void launch_product(const BlockPlan& b, const BlockOps& p, const BlockOut& o, hipStream_t s) {
+  if (b.skinny) return launch_skinny<ROWB, O>(b, p, o, s);
+  if constexpr (EXACT) {
+    launch_tiles<2, ROWB, FragF16, O>(b, p, o, s);
+  } else {
+    if constexpr (!ROWB)
+      if (b.nj == 4) return launch_tiles<4, ROWB, FragFp8, O>(b, p, o, s);
+    launch_tiles<2, ROWB, FragFp8, O>(b, p, o, s);
+  }
+}
+
+unsigned sweep_blocks(int64_t n) { return (unsigned)(ceil_div(n, 256) < 8192 ? ceil_div(n, 256) : 8192); }
+
+template <class O>
+hipError_t run_matmul(const stce_block_matmul& p, void* ws, hipStream_t s) {
+  constexpr bool EXACT = sizeof(O) == 4;
   ProfScope ps(KIND_BLOCK_MATMUL, s);
-  hipLaunchKernelGGL(block_matmul_simple_kernel<O>, dim3((unsigned)ceil_div(p.N, 16), (unsigned)ceil_div(p.M, 16)),
-                     dim3(64), 0, s, p);
+  if (p.K == 0) {
+    if (!p.accumulate)
+      hipLaunchKernelGGL(block_zero_kernel<O>, dim3(sweep_blocks(p.M * p.N)), dim3(256), 0, s, p.M, p.N, (O*)p.out,
+                         p.ldo);
+    return hipGetLastError();
+  }
+  const BlockPlan b = plan_product(p);
+  const BlockOps ops{p.a,           p.b,           p.a_scale,          p.b_scale,          p.lda,    p.ldb,
+                     p.a_block_stride, p.b_block_stride, (int)p.a_row_stride, (int)p.b_row_stride, (int)p.M, (int)p.N,
+                     (int)p.K};
+  const bool rowb = p.b_rows == 1;
+  if (b.S == 1) {
+    const BlockOut o{p.out, p.ldo, 0, p.accumulate};
+    if (rowb)
+      launch_product<true, O, EXACT>(b, ops, o, s);
+    else
+      launch_product<false, O, EXACT>(b, ops, o, s);
+    return hipGetLastError();
+  }
+  const BlockOut o{ws, p.N, p.M * p.N, 0};
+  if (rowb)
+    launch_product<true, float, EXACT>(b, ops, o, s);
+  else
+    launch_product<false, float, EXACT>(b, ops, o, s);
+  const hipError_t e = hipGetLastError();
+  if (e) return e;
+  hipLaunchKernelGGL(block_sum_kernel<O>, dim3(sweep_blocks(p.M * p.N)), dim3(256), 0, s, (const float*)ws, b.S, p.M,
+                     p.N, (O*)p.out, p.ldo, p.accumulate);
   return hipGetLastError();
 }
 
@@ -169,13 +384,17 @@ hipError_t launch_quantize_blocks(const void* x, int dtype, int64_t R, int64_t C
   }
 }
 
-size_t block_matmul_workspace_bytes(const stce_block_matmul&) { return 0; }
+size_t block_matmul_workspace_bytes(const stce_block_matmul& p) {
+  if (p.K == 0) return 0;
+  const BlockPlan b = plan_product(p);
+  return b.S > 1 ? sizeof(float) * (size_t)b.S * (size_t)p.M * (size_t)p.N : 0;
+}
 
-hipError_t launch_block_matmul(const stce_block_matmul& p, void*, hipStream_t s) {
+hipError_t launch_block_matmul(const stce_block_matmul& p, void* ws, hipStream_t s) {
   switch (p.out_dtype) {
-    case STCE_DT_BF16: return run_matmul<bf16>(p, s);
-    case STCE_DT_F16: return run_matmul<_Float16>(p, s);
-    default: return run_matmul<float>(p, s);
+    case STCE_DT_BF16: return run_matmul<bf16>(p, ws, s);
+    case STCE_DT_F16: return run_matmul<_Float16>(p, ws, s);
+    default: return run_matmul<float>(p, ws, s);
   }
 }
 

@@ -95,6 +95,12 @@ stce_status check_matmul_shapes(const stce_block_matmul* p) {
     return fail(STCE_E_ARG, "b_rows=%d: one scale per 1 or 128 rows of b", (int)p->b_rows);
   if (p->a_row_stride < 0 || p->a_block_stride < 0 || p->b_row_stride < 0 || p->b_block_stride < 0)
     return fail(STCE_E_ARG, "scale strides must be >= 0");
+  // (the rows of a tile's scales are addressed with 32-bit byte offsets)
+  if (p->a_row_stride > (1 << 20) || p->b_row_stride > (1 << 20))
+    return fail(STCE_E_UNSUPPORTED, "scale row strides must be at most 2^20 elements");
+  // (the launch: one workgroup per 16 x M or 256 x 64 outputs)
+  if (p->M > 64 && ceil_div(p->M, 64) * ceil_div(p->N, 256) > INT32_MAX / 2)
+    return fail(STCE_E_UNSUPPORTED, "M=%lld x N=%lld has too many output tiles", (long long)p->M, (long long)p->N);
   if (p->accumulate && p->out_dtype != STCE_DT_F32)
     return fail(STCE_E_UNSUPPORTED, "accumulate takes an fp32 output");
   return STCE_OK;
