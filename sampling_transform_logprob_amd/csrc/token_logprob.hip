@@ -159,31 +159,318 @@ __device__ inline void write_row(const RowOut& r, const Z* z, int64_t t, float t
   }
 }
 
-// One workgroup per row, three passes over it: maximum, sums, alternatives.
+// 16 bytes of a row as fp32 values (rows need no more than their element's
+// alignment: the loads are unaligned where the row is).
 template <class Z>
-__global__ __launch_bounds__(TW) void token_row_kernel(const Z* logits, int64_t ld, const float* temperature,
-                                                       RowOut r) {
-  __shared__ TopScratch top;
-  __shared__ float red[TW / 64];
-  const int64_t t = blockIdx.x;
+struct Granule {
+  static constexpr int E = 16 / sizeof(Z);
+  struct __attribute__((packed, aligned(sizeof(Z)))) Raw {
+    Z v[E];
+  };
+};
+
+template <class Z>
+__device__ inline void load_granule(const Z* z, int64_t j, int64_t V, float* x) {
+  constexpr int E = Granule<Z>::E;
+  if (j + E <= V) {
+    const typename Granule<Z>::Raw r = *(const typename Granule<Z>::Raw*)(z + j);
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = to_f32(r.v[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = j + e < V ? to_f32(z[j + e]) : NEG_INF;
+  }
+}
+
+// Order keys of a logit type's values: the low SHIFT bits of the fp32 image
+// say nothing (zeros, or ones below zero), so a search skips them.
+template <class Z>
+struct KeyShift;
+template <>
+struct KeyShift<bf16> {
+  static constexpr int SHIFT = 16;
+};
+template <>
+struct KeyShift<_Float16> {
+  static constexpr int SHIFT = 13;
+};
+template <>
+struct KeyShift<float> {
+  static constexpr int SHIFT = 0;
+};
+constexpr uint32_t KEY_LOWEST = 0x00800000u;  // of the lowest finite value; -inf lies one below
+
+// The largest multiple k of 2^SHIFT such that at least n of the wave's 64 NK
+// keys reach k (all of them reach 0).
+template <int SHIFT, int NK>
+__device__ inline uint32_t nth_key(const uint32_t (&key)[NK], int n) {
+  uint32_t k = 0;
+#pragma unroll
+  for (int b = 31; b >= SHIFT; --b) {
+    const uint32_t t = k | (1u << b);
+    int cnt = 0;
+#pragma unroll
+    for (int q = 0; q < NK; ++q) cnt += __popcll(__ballot(key[q] >= t));
+    k = cnt >= n ? t : k;
+  }
+  return k;
+}
+
+// Maximum and sums of a part of a row relative to that maximum.
+struct Partial {
+  float m, S, E, pad;
+};
+
+// Re-bases (S, E) from maximum m to the maximum of m and mn; returns it.
+__device__ inline void rebase(float& m, float& S, float& E, float mn, float c) {
+  const float ref = mn == NEG_INF ? 0.0f : mn;
+  const float d = fmaxf((m - ref) * c, -200.0f);  // (2^-200 is 0: an empty part has S = 0)
+  const float r = exp2_fast(d);
+  E = r * __builtin_fmaf(S, d, E);
+  S *= r;
+  m = mn;
+}
+
+struct SegmentPlan {
+  int segs;            // workgroups per row
+  int tiles;           // tiles of a row
+  int tps;             // tiles per segment
+  int tpc;             // tiles per cell (see below)
+};
+
+constexpr int CELLS = 16;      // cells of a thread at most
+constexpr int CELL_CAP = 512;  // cells that may hold alternatives
+
+// One workgroup per segment of a row, one pass over it: a tile is EPT elements
+// a thread, 16 bytes at a time, all in flight at once; each thread keeps its
+// own running maximum and sums, so the loop has no barrier.
+//
+// Alternatives cost the loop one LDS write per cell, a cell being a thread's
+// elements of tpc consecutive tiles: its maximum.  The n-th largest of the 256
+// threads' maxima is a lower bound of the n-th largest element, and little more
+// than n elements reach it (20.8 expected of 8,192 random ones for n = 20), so
+// after the loop only the cells that reach the bound are read again and their
+// elements above it ranked.  Rows whose ties overflow the lists take scan_top.
+template <class Z, int EPT, bool TOP>
+__global__ __launch_bounds__(TW) void token_segment_kernel(const Z* logits, int64_t ld, const float* temperature,
+                                                           RowOut r, SegmentPlan pl, Partial* part, uint64_t* tops) {
+  constexpr int E = Granule<Z>::E, NG = EPT / E, TILE = TW * EPT;
+  extern __shared__ float cells[];  // [cells][TW] with TOP
+  __shared__ Partial red[TW / 64];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int64_t t = blockIdx.x / pl.segs;
+  const int seg = blockIdx.x - (int)t * pl.segs;
+  const int t0 = seg * pl.tps, t1 = min(t0 + pl.tps, pl.tiles);
   const Z* z = logits + t * ld;
   const float temp = temperature ? temperature[t] : 1.0f;
   const float c = inv_temperature(temp);
-  float m = NEG_INF;
-  for (int64_t j = threadIdx.x; j < r.V; j += TW) m = fmaxf(m, to_f32(z[j]));
-  m = block_reduce<true>(m, red);
-  const float ref = m == NEG_INF ? 0.0f : m;
-  float S = 0.0f, E = 0.0f;
-  for (int64_t j = threadIdx.x; j < r.V; j += TW) {
-    const float x = (to_f32(z[j]) - ref) * c;
-    const float e = exp2_fast(x);
-    S += e;
-    E = __builtin_fmaf(e, fmaxf(x, -200.0f), E);
+  float m = NEG_INF, S = 0.0f, Es = 0.0f, cmax = NEG_INF;
+  int cell = 0, in_cell = 0;
+  for (int tile = t0; tile < t1; ++tile) {
+    const int64_t j0 = (int64_t)tile * TILE + tid * E;
+    float x[EPT];
+    if ((int64_t)(tile + 1) * TILE <= r.V) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const typename Granule<Z>::Raw raw = *(const typename Granule<Z>::Raw*)(z + j0 + g * TW * E);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[g * E + e] = to_f32(raw.v[e]);
+      }
+    } else {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) load_granule(z, j0 + g * TW * E, r.V, x + g * E);
+    }
+    float mx = x[0];
+#pragma unroll
+    for (int e = 1; e < EPT; ++e) mx = fmaxf(mx, x[e]);
+    if constexpr (TOP) {
+      cmax = fmaxf(cmax, mx);
+      if (++in_cell == pl.tpc || tile + 1 == t1) {
+        cells[cell * TW + tid] = cmax;
+        ++cell;
+        in_cell = 0;
+        cmax = NEG_INF;
+      }
+    }
+    rebase(m, S, Es, fmaxf(m, mx), c);
+    const float ref = m == NEG_INF ? 0.0f : m;
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) {
+      const float d = (x[e] - ref) * c;
+      const float p = exp2_fast(d);
+      S += p;
+      Es = __builtin_fmaf(p, fmaxf(d, -200.0f), Es);
+    }
   }
-  S = block_reduce<false>(S, red);
-  E = block_reduce<false>(E, red);
-  if (r.top_n) scan_top(z, 0, r.V, r.top_n, top);
-  write_row(r, z, t, temp, m, S, E, top.sorted, threadIdx.x, TW);
+  const float mine = m;  // (a NaN does not reach it)
+  // join the threads: lanes, then waves, each in a fixed order
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const float om = __shfl_xor(m, o);
+    rebase(m, S, Es, fmaxf(m, om), c);
+    S += __shfl_xor(S, o);
+    Es += __shfl_xor(Es, o);
+  }
+  if (lane == 0) red[w] = Partial{m, S, Es, 0.0f};
+  __shared__ TopScratch top_s;
+  TopScratch& top = top_s;
+  __shared__ float tmax[TOP ? TW : 1];
+  __shared__ uint16_t list[TOP ? CELL_CAP : 1];
+  __shared__ int ncell;
+  if constexpr (TOP) {
+    tmax[tid] = mine;
+    if (tid == 0) {
+      ncell = 0;
+      top.count = 0;
+    }
+  }
+  __syncthreads();
+  float M = red[0].m;
+#pragma unroll
+  for (int i = 1; i < TW / 64; ++i) M = fmaxf(M, red[i].m);
+  S = Es = 0.0f;
+#pragma unroll
+  for (int i = 0; i < TW / 64; ++i) {
+    float pm = red[i].m, pS = red[i].S, pE = red[i].E;
+    rebase(pm, pS, pE, M, c);
+    S += pS;
+    Es += pE;
+  }
+  if constexpr (TOP) {
+    const int n = r.top_n;
+    uint32_t key[TW / 64];
+#pragma unroll
+    for (int q = 0; q < TW / 64; ++q) key[q] = order_key(tmax[q * 64 + lane]);
+    uint32_t bar = nth_key<KeyShift<Z>::SHIFT>(key, n);
+    bar = bar < KEY_LOWEST ? KEY_LOWEST : bar;
+    for (int i = 0; i < cell; ++i) {
+      if (order_key(cells[i * TW + tid]) >= bar) {
+        const int at = atomicAdd(&ncell, 1);
+        if (at < CELL_CAP) list[at] = (uint16_t)(i * TW + tid);
+      }
+    }
+    __syncthreads();
+    const int nc = ncell;
+    if (nc <= CELL_CAP) {
+      const int per = pl.tpc * NG;
+      for (int i = tid; i < nc * per; i += TW) {
+        const int ci = list[i / per], q = i % per;
+        const int tile = t0 + ci / TW * pl.tpc + q / NG;
+        const int64_t j = (int64_t)tile * TILE + (q % NG) * TW * E + (ci % TW) * E;
+        if (tile >= t1 || j >= r.V) continue;
+        float x[E];
+        load_granule(z, j, r.V, x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const uint32_t k = order_key(x[e]);
+          if (k >= bar && x[e] > NEG_INF) {
+            const int at = atomicAdd(&top.count, 1);
+            if (at < LIST_CAP) top.list[at] = composite(k, (uint32_t)(j + e));
+          }
+        }
+      }
+      __syncthreads();
+    }
+    if (nc <= CELL_CAP && top.count <= LIST_CAP) {
+      rank_list(top, n);
+    } else {
+      __syncthreads();
+      const int64_t j1 = (int64_t)t1 * TILE;
+      scan_top(z, (int64_t)t0 * TILE, j1 < r.V ? j1 : r.V, n, top);
+    }
+    if (part)
+      for (int i = tid; i < n; i += TW) tops[(size_t)blockIdx.x * n + i] = top.sorted[i];
+  }
+  if (!part) {
+    write_row(r, z, t, temp, M, S, Es, top.sorted, tid, TW);
+  } else if (tid == 0) {
+    part[blockIdx.x] = Partial{M, S, Es, 0.0f};
+  }
+}
+
+constexpr int JOIN_CAP = 1024;  // alternatives of a row's segments together
+
+// One wave per row: its segments' partial statistics and alternatives joined.
+template <class Z, bool TOP>
+__global__ __launch_bounds__(64) void token_join_kernel(const Z* logits, int64_t ld, const float* temperature,
+                                                        RowOut r, int segs, const Partial* part,
+                                                        const uint64_t* tops) {
+  __shared__ uint64_t list[TOP ? JOIN_CAP : 1];
+  __shared__ uint64_t sorted[TOP_MAX];
+  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x;
+  const float temp = temperature ? temperature[t] : 1.0f;
+  const float c = inv_temperature(temp);
+  float m = NEG_INF, S = 0.0f, Es = 0.0f;
+  for (int s = lane; s < segs; s += 64) {
+    const Partial p = part[t * segs + s];
+    float pm = p.m, pS = p.S, pE = p.E;
+    const float mn = fmaxf(m, pm);
+    rebase(m, S, Es, mn, c);
+    rebase(pm, pS, pE, mn, c);
+    S += pS;
+    Es += pE;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const float om = __shfl_xor(m, o);
+    rebase(m, S, Es, fmaxf(m, om), c);
+    S += __shfl_xor(S, o);
+    Es += __shfl_xor(Es, o);
+  }
+  if constexpr (TOP) {
+    const int n = r.top_n, total = segs * n;  // <= JOIN_CAP
+    uint64_t v[JOIN_CAP / 64];
+    uint32_t key[JOIN_CAP / 64];
+#pragma unroll
+    for (int q = 0; q < JOIN_CAP / 64; ++q) {
+      v[q] = q * 64 + lane < total ? tops[(size_t)t * total + q * 64 + lane] : 0;
+      key[q] = comp_key(v[q]);
+    }
+    uint32_t bar = nth_key<KeyShift<Z>::SHIFT>(key, n);
+    bar = bar < KEY_LOWEST ? KEY_LOWEST : bar;
+    int cnt = 0;
+#pragma unroll
+    for (int q = 0; q < JOIN_CAP / 64; ++q) {
+      const uint64_t hit = __ballot(key[q] >= bar);
+      if (key[q] >= bar) list[cnt + __popcll(hit & ((1ull << lane) - 1))] = v[q];
+      cnt += __popcll(hit);
+    }
+    __syncthreads();
+    for (int i = lane; i < n; i += 64)
+      if (i >= cnt) sorted[i] = 0;
+    for (int i = lane; i < cnt; i += 64) {
+      const uint64_t mine = list[i];
+      int rank = 0;
+      for (int j = 0; j < cnt; ++j) rank += list[j] > mine ? 1 : 0;
+      if (rank < n) sorted[rank] = mine;
+    }
+    __syncthreads();
+  }
+  write_row(r, logits + t * ld, t, temp, m, S, Es, sorted, lane, 64);
+}
+
+// How rows are cut: tiles of 8,192 elements where the rows fill the chip, of
+// 2,048 elsewhere (a short row's latency is its loads' and the lists'); about
+// 1,024 workgroups in all, as long as a row's segments' alternatives fit the
+// joining wave.
+struct TokenPlan {
+  bool wide;
+  SegmentPlan s;
+};
+TokenPlan plan_tokens(const stce_token_problem& p) {
+  TokenPlan t{};
+  t.wide = p.T * ceil_div(p.V, 8192) >= 1024;
+  const int64_t tiles = ceil_div(p.V, t.wide ? 8192 : 2048);
+  int64_t segs = ceil_div(1024, p.T);
+  if (segs > tiles) segs = tiles;
+  if (p.top_n && segs > JOIN_CAP / p.top_n) segs = JOIN_CAP / p.top_n;
+  const int64_t tps = ceil_div(tiles, segs);
+  t.s.segs = (int)ceil_div(tiles, tps);
+  t.s.tiles = (int)tiles;
+  t.s.tps = (int)tps;
+  t.s.tpc = (int)ceil_div(tps, CELLS);
+  return t;
 }
 
 // Gradient of the logits, one workgroup per row.
@@ -230,14 +517,39 @@ RowOut row_out(const stce_token_problem& p, const stce_token_outputs& o, int64_t
   return RowOut{o, p.tokens, p.V, p.ignore_index, p.K, p.top_n, p.flags & STCE_PROBLEM_IGNORE_INDEX, status};
 }
 
+template <class Z, int EPT, bool TOP>
+void launch_segments(const TokenPlan& pl, const stce_token_problem& p, const RowOut& r, Partial* part, uint64_t* tops,
+                     hipStream_t s) {
+  const size_t lds = TOP ? sizeof(float) * TW * (size_t)ceil_div(pl.s.tps, pl.s.tpc) : 0;
+  hipLaunchKernelGGL((token_segment_kernel<Z, EPT, TOP>), dim3((unsigned)(p.T * pl.s.segs)), dim3(TW), lds, s,
+                     (const Z*)p.logits, p.ld, p.temperature, r, pl.s, part, tops);
+}
+
+template <class Z, bool TOP>
+hipError_t run_forward_as(const stce_token_problem& p, const RowOut& r, void* ws, hipStream_t s) {
+  const TokenPlan pl = plan_tokens(p);
+  Partial* part = pl.s.segs > 1 ? (Partial*)ws : nullptr;
+  uint64_t* tops = part ? (uint64_t*)(part + p.T * pl.s.segs) : nullptr;
+  {
+    ProfScope ps(KIND_TOKEN_LOGPROBS, s);
+    if (pl.wide)
+      launch_segments<Z, 32, TOP>(pl, p, r, part, tops, s);
+    else
+      launch_segments<Z, 8, TOP>(pl, p, r, part, tops, s);
+  }
+  hipError_t e = hipGetLastError();
+  if (e || !part) return e;
+  ProfScope ps(KIND_TOKEN_MERGE, s);
+  hipLaunchKernelGGL((token_join_kernel<Z, TOP>), dim3((unsigned)p.T), dim3(64), 0, s, (const Z*)p.logits, p.ld,
+                     p.temperature, r, pl.s.segs, part, tops);
+  return hipGetLastError();
+}
+
 template <class Z>
-hipError_t run_forward(const stce_token_problem& p, const stce_token_outputs& o, int64_t* status, void*,
+hipError_t run_forward(const stce_token_problem& p, const stce_token_outputs& o, int64_t* status, void* ws,
                        hipStream_t s) {
   const RowOut r = row_out<Z>(p, o, status);
-  ProfScope ps(KIND_TOKEN_LOGPROBS, s);
-  hipLaunchKernelGGL(token_row_kernel<Z>, dim3((unsigned)p.T), dim3(TW), 0, s, (const Z*)p.logits, p.ld,
-                     p.temperature, r);
-  return hipGetLastError();
+  return r.top_n ? run_forward_as<Z, true>(p, r, ws, s) : run_forward_as<Z, false>(p, r, ws, s);
 }
 
 template <class Z>
@@ -251,7 +563,11 @@ hipError_t run_grad(const stce_token_problem& p, const TokenStats* stats, const 
 
 }  // namespace
 
-size_t token_workspace_bytes(const stce_token_problem&) { return 0; }
+size_t token_workspace_bytes(const stce_token_problem& p) {
+  const TokenPlan pl = plan_tokens(p);
+  if (pl.s.segs == 1) return 0;
+  return (size_t)p.T * pl.s.segs * (sizeof(Partial) + sizeof(uint64_t) * (size_t)p.top_n);
+}
 
 hipError_t launch_token_logprobs(const stce_token_problem& p, const stce_token_outputs& o, int64_t* status, void* ws,
                                  hipStream_t s) {
