@@ -473,42 +473,103 @@ TokenPlan plan_tokens(const stce_token_problem& p) {
   return t;
 }
 
-// Gradient of the logits, one workgroup per row.
-template <class Z>
+// Gradient of the logits: dz_j = (p_j (a0 - a1 x_j) + the given tokens' terms) / T
+// with x_j = log2 p_j, p_j = 2^x_j, a0 = grad_lse - sum g - grad_entropy H and
+// a1 = ln 2 grad_entropy.  One read and one write of the row, 16 bytes a
+// thread at a time; a workgroup takes `tiles` tiles of 4 granules a thread.
+//
+// A given token's gradient is added by the thread that holds its element, before
+// the one rounding: the granules that hold given tokens are marked first (one bit
+// a granule, tiles x 4 <= 32 of a thread), and a marked granule's thread looks
+// through the row's tokens in order, so a token given twice gets both and equal
+// calls give equal bits.
+constexpr int GRAD_NG = 4, GRAD_TILES = 8;  // granules a thread and tile; tiles a workgroup at most
+
+template <class Z, bool FEW>
 __global__ __launch_bounds__(TW) void token_grad_kernel(const Z* logits, int64_t ld, const float* temperature,
                                                         const TokenStats* stats, const int64_t* tokens, int K,
                                                         int64_t V, const float* g_lp, const float* g_ent,
-                                                        const float* g_lse, Z* grad, int64_t ld_grad) {
+                                                        const float* g_lse, Z* grad, int64_t ld_grad, int segs,
+                                                        int tiles) {
+  constexpr int E = Granule<Z>::E, TILE = TW * E * GRAD_NG;
+  constexpr int CAP = FEW ? 8 : TOKENS_MAX;
+  typedef typename Granule<Z>::Raw Raw;
   __shared__ float red[TW / 64];
-  __shared__ int32_t tok[TOKENS_MAX];
-  __shared__ float tg[TOKENS_MAX];
-  const int64_t t = blockIdx.x;
+  __shared__ uint32_t mark[TW];
+  __shared__ int32_t tok[CAP];
+  __shared__ float tg[CAP];
+  const int tid = threadIdx.x;
+  const int64_t t = blockIdx.x / segs;
+  const int64_t j0 = (int64_t)(blockIdx.x - (int)t * segs) * tiles * TILE;
+  const int64_t j1 = j0 + (int64_t)tiles * TILE < V ? j0 + (int64_t)tiles * TILE : V;
   const Z* z = logits + t * ld;
   Z* dz = grad + t * ld_grad;
   const float temp = temperature ? temperature[t] : 1.0f;
   const TokenStats st = stats[t];
-  if (bad_temperature(temp) || !(st.m > NEG_INF && st.m < __builtin_huge_valf()) || st.log_sum != st.log_sum) {
-    for (int64_t j = threadIdx.x; j < V; j += TW) dz[j] = (Z)0.0f;
-    return;
-  }
+  const bool none =
+      bad_temperature(temp) || !(st.m > NEG_INF && st.m < __builtin_huge_valf()) || st.log_sum != st.log_sum;
   const float c = inv_temperature(temp), l2 = st.log_sum * LOG2E;
+  const float rt = fminf(1.0f / temp, 3.4028235e38f);
+  mark[tid] = 0;
+  __syncthreads();
   float g = 0.0f;
-  for (int i = threadIdx.x; i < K; i += TW) {
-    const int64_t y = tokens[t * K + i];
-    const bool ok = y >= 0 && y < V && g_lp && to_f32(z[y]) > NEG_INF;
-    tok[i] = ok ? (int32_t)y : -1;
-    tg[i] = ok ? g_lp[t * K + i] : 0.0f;
-    g += tg[i];
+  if (g_lp) {
+    for (int i = tid; i < K; i += TW) {
+      const int64_t y = tokens[t * K + i];
+      const bool ok = y >= 0 && y < V && to_f32(z[y]) > NEG_INF;
+      const float v = ok ? g_lp[t * K + i] : 0.0f;
+      tok[i] = ok ? (int32_t)y : -1;
+      tg[i] = v;
+      g += v;
+      if (ok && y >= j0 && y < j1) {
+        const int64_t at = y - j0, in = at % TILE;
+        atomicOr(&mark[in / E % TW], 1u << (int)(at / TILE * GRAD_NG + in / (E * TW)));
+      }
+    }
+    g = block_reduce<false>(g, red);  // (its barriers make the marks and tokens visible)
   }
-  g = block_reduce<false>(g, red);
   const float ge = g_ent ? g_ent[t] : 0.0f, gl = g_lse ? g_lse[t] : 0.0f;
-  const float a0 = (gl - g - ge * st.entropy) / temp, a1 = ge * LN2 / temp;
-  for (int64_t j = threadIdx.x; j < V; j += TW) {
-    const float x = fmaxf((to_f32(z[j]) - st.m) * c - l2, -200.0f);
-    float d = exp2_fast(x) * __builtin_fmaf(-a1, x, a0);
-    float own = 0.0f;
-    for (int i = 0; i < K; ++i) own += tok[i] == (int32_t)j ? tg[i] : 0.0f;
-    dz[j] = (Z)(d + own / temp);
+  const float a0 = gl - g - ge * st.entropy, a1 = ge * LN2;
+  const uint32_t marks = mark[tid];
+  auto one = [&](Z v) __attribute__((always_inline)) {
+    const float x = fmaxf((to_f32(v) - st.m) * c - l2, -200.0f);
+    return none ? 0.0f : exp2_fast(x) * __builtin_fmaf(-a1, x, a0) * rt;
+  };
+  auto given = [&](int64_t j) __attribute__((always_inline)) {
+    float v = 0.0f;
+    for (int i = 0; i < K; ++i) v += tok[i] == (int32_t)j ? tg[i] : 0.0f;
+    return none ? 0.0f : v * rt;
+  };
+  for (int tile = 0; tile < tiles; ++tile) {
+    const int64_t b = j0 + (int64_t)tile * TILE + tid * E;
+    if (j0 + (int64_t)tile * TILE >= j1) break;
+    if (j0 + (int64_t)(tile + 1) * TILE <= V) {
+      Raw in[GRAD_NG];
+#pragma unroll
+      for (int q = 0; q < GRAD_NG; ++q) in[q] = *(const Raw*)(z + b + q * TW * E);
+#pragma unroll
+      for (int q = 0; q < GRAD_NG; ++q) {
+        float d[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) d[e] = one(in[q].v[e]);
+        if (marks >> (tile * GRAD_NG + q) & 1) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) d[e] += given(b + q * TW * E + e);
+        }
+        Raw o;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o.v[e] = (Z)d[e];
+        *(Raw*)(dz + b + q * TW * E) = o;
+      }
+    } else {
+      for (int q = 0; q < GRAD_NG; ++q) {
+        const bool marked = marks >> (tile * GRAD_NG + q) & 1;
+        for (int e = 0; e < E; ++e) {
+          const int64_t j = b + q * TW * E + e;
+          if (j < V) dz[j] = (Z)(one(z[j]) + (marked ? given(j) : 0.0f));
+        }
+      }
+    }
   }
 }
 
@@ -555,9 +616,21 @@ hipError_t run_forward(const stce_token_problem& p, const stce_token_outputs& o,
 template <class Z>
 hipError_t run_grad(const stce_token_problem& p, const TokenStats* stats, const float* g_lp, const float* g_ent,
                     const float* g_lse, void* grad, int64_t ld_grad, hipStream_t s) {
+  // as many tiles a workgroup as leave about 2,048 workgroups
+  const int64_t all = ceil_div(p.V, (int64_t)TW * Granule<Z>::E * GRAD_NG);
+  int64_t tiles = all * p.T / 2048;
+  tiles = tiles < 1 ? 1 : tiles > GRAD_TILES ? GRAD_TILES : tiles;
+  if (tiles > all) tiles = all;
+  const int64_t segs = ceil_div(all, tiles);
   ProfScope ps(KIND_TOKEN_GRAD, s);
-  hipLaunchKernelGGL(token_grad_kernel<Z>, dim3((unsigned)p.T), dim3(TW), 0, s, (const Z*)p.logits, p.ld,
-                     p.temperature, stats, p.tokens, p.K, p.V, g_lp, g_ent, g_lse, (Z*)grad, ld_grad);
+  const auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(p.T * segs)), dim3(TW), 0, s, (const Z*)p.logits, p.ld, p.temperature,
+                       stats, p.tokens, p.K, p.V, g_lp, g_ent, g_lse, (Z*)grad, ld_grad, (int)segs, (int)tiles);
+  };
+  if (p.K <= 8)
+    launch(token_grad_kernel<Z, true>);
+  else
+    launch(token_grad_kernel<Z, false>);
   return hipGetLastError();
 }
 
