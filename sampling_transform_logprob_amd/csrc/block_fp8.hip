@@ -38,45 +38,145 @@ __device__ inline float mag(float v) {
   return x < __builtin_huge_valf() ? x : __builtin_huge_valf();
 }
 
-// One workgroup per block (128 columns of one row of Y, or a 128 x 128 tile):
-// element (q, l) of Y is x[q * sq + l * sl].
-template <class X, bool TILE>
-__global__ __launch_bounds__(128) void quantize_simple_kernel(const X* x, int64_t sq, int64_t sl, int64_t Q, int64_t L,
-                                                              uint8_t* codes, int64_t ld, float* scales) {
-  __shared__ float red[2];
-  const int64_t qb = blockIdx.x, lb = blockIdx.y;
-  const int64_t q0 = TILE ? qb * QB : qb, q1 = TILE ? (q0 + QB < Q ? q0 + QB : Q) : q0 + 1;
-  const int64_t l = lb * QB + threadIdx.x;
-  float mx = 0.0f;
-  if (l < L)
-    for (int64_t q = q0; q < q1; ++q) mx = fmaxf(mx, mag((float)x[q * sq + l * sl]));
+__device__ inline uint32_t encode2(float lo, float hi, uint32_t old, bool upper) {
+  return upper ? __builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, (int)old, true)
+               : __builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, (int)old, false);
+}
+
+// Eight neighbouring elements of a row of x.
+template <class X>
+struct __attribute__((packed, aligned(sizeof(X)))) Eight {
+  X v[8];
+};
+
+// A workgroup of 256 threads quantizes 128 x 128 elements of x, held in
+// registers between the maximum and the codes: thread t has columns 8 (t % 16)
+// .. + 8 of rows t / 16 + 16 i, i < 8.  One read of x, one write of codes.
+//   scale per row and 128 columns (ROWS):     maximum over 16 lanes
+//   scale per column and 128 rows (COLUMNS):  over a thread's rows, 4 lanes, 4 waves
+//   scale per tile (TILE):                    over the workgroup
+// With TR the codes are written transposed, through LDS (rows of 128 + 16 bytes:
+// 16-byte reads of a column's codes), else 8 bytes a thread.
+// The codes come from the hardware's conversion to e4m3 (nearest, ties to
+// even).
+enum : int { Q_ROWS = 0, Q_COLUMNS = 1, Q_TILE = 2 };
+template <class X, int MODE, bool TR>
+__global__ __launch_bounds__(256) void quantize_kernel(const X* x, int64_t ld, int64_t R, int64_t C, uint8_t* codes,
+                                                       int64_t ldc, float* scales) {
+  constexpr int LDT = QB + 16;
+  __shared__ float red[MODE == Q_COLUMNS ? 4 * QB : 4];
+  __shared__ __attribute__((aligned(16))) uint8_t tile[TR ? QB * LDT : 16];
+  const int tid = threadIdx.x, tc = tid & 15, tr = tid >> 4;
+  // (neighbouring workgroups share rows of x)
+  const int64_t cbs = (C + QB - 1) / QB;
+  const int64_t rb = blockIdx.x / cbs, cb = blockIdx.x - rb * cbs;
+  const int64_t c0 = cb * QB + tc * 8;
+  float v[8][8];
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = mx;
-  __syncthreads();
-  const BlockScale b = block_scale(fmaxf(red[0], red[1]));
-  if (threadIdx.x == 0) scales[lb * (TILE ? ceil_div(Q, QB) : Q) + qb] = b.a;
-  if (l < round_up(L, 16))
-    for (int64_t q = q0; q < q1; ++q) {
-      uint32_t c = 0;
-      if (l < L && b.finite) c = e4m3_encode(scaled_value((float)x[q * sq + l * sl], b.a, b.r, b.ok));
-      codes[q * ld + l] = (uint8_t)c;
+  for (int i = 0; i < 8; ++i) {
+    const int64_t r = rb * QB + tr + 16 * i;
+    if (r < R && c0 + 8 <= C) {
+      const Eight<X> e = *(const Eight<X>*)(x + r * ld + c0);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[i][k] = (float)e.v[k];
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[i][k] = r < R && c0 + k < C ? (float)x[r * ld + c0 + k] : 0.0f;
     }
+  }
+  auto lanes = [](float m, int from, int to) {
+    for (int o = from; o < to; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
+    return m;
+  };
+  BlockScale s[MODE == Q_TILE ? 1 : 8];  // of the thread's rows, columns, or the tile
+  if constexpr (MODE == Q_ROWS) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float m = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = fmaxf(m, mag(v[i][k]));
+      s[i] = block_scale(lanes(m, 1, 16));
+      const int64_t r = rb * QB + tr + 16 * i;
+      if (tc == 0 && r < R) scales[cb * R + r] = s[i].a;
+    }
+  } else if constexpr (MODE == Q_COLUMNS) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, mag(v[i][k]));
+      m = lanes(m, 16, 64);
+      if ((tid & 63) < 16) red[(tid >> 6) * QB + tc * 8 + k] = m;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float m = red[tc * 8 + k];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) m = fmaxf(m, red[w * QB + tc * 8 + k]);
+      s[k] = block_scale(m);
+      if (tr == 0 && c0 + k < C) scales[rb * C + c0 + k] = s[k].a;
+    }
+  } else {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = fmaxf(m, mag(v[i][k]));
+    m = lanes(m, 1, 64);
+    if ((tid & 63) == 0) red[tid >> 6] = m;
+    __syncthreads();
+    s[0] = block_scale(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
+    // (scales [blocks of the reduction][tiles of the other])
+    if (tid == 0) scales[TR ? rb * cbs + cb : cb * ((R + QB - 1) / QB) + rb] = s[0].a;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      float q[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const BlockScale& b = s[MODE == Q_ROWS ? i : MODE == Q_COLUMNS ? k + h : 0];
+        q[h] = b.finite ? scaled_value(v[i][k + h], b.a, b.r, b.ok) : 0.0f;
+      }
+      w[k >> 2] = encode2(q[0], q[1], w[k >> 2], k & 2);
+    }
+    const int row = tr + 16 * i;
+    if constexpr (TR) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) tile[(tc * 8 + k) * LDT + row] = (uint8_t)(w[k >> 2] >> (8 * (k & 3)));
+    } else {
+      const int64_t r = rb * QB + row;
+      if (r < R && c0 < (C + 15) / 16 * 16) *(u32x2*)(codes + r * ldc + c0) = u32x2{w[0], w[1]};
+    }
+  }
+  if constexpr (TR) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int ch = i * 256 + tid, c = ch >> 3, r16 = (ch & 7) * 16;
+      const int64_t col = cb * QB + c, row = rb * QB + r16;
+      if (col < C && row < (R + 15) / 16 * 16)
+        *(u32x4*)(codes + col * ldc + row) = *(const u32x4*)(tile + c * LDT + r16);
+    }
+  }
 }
 
 template <class X>
 hipError_t run_quantize(const X* x, int64_t R, int64_t C, int64_t ld, int flags, uint8_t* codes, int64_t ld_codes,
                         float* scales, hipStream_t s) {
   const bool tr = flags & STCE_QUANT_TRANSPOSE, tile = flags & STCE_QUANT_TILE;
-  const int64_t Q = tr ? C : R, L = tr ? R : C, sq = tr ? 1 : ld, sl = tr ? ld : 1;
-  const dim3 grid((unsigned)(tile ? ceil_div(Q, QB) : Q), (unsigned)ceil_div(L, QB));
+  const dim3 grid((unsigned)(ceil_div(R, QB) * ceil_div(C, QB)));
   ProfScope ps(KIND_QUANTIZE_BLOCKS, s);
+  const auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, x, ld, R, C, codes, ld_codes, scales);
+  };
   if (tile)
-    hipLaunchKernelGGL((quantize_simple_kernel<X, true>), grid, dim3(128), 0, s, x, sq, sl, Q, L, codes, ld_codes,
-                       scales);
+    tr ? launch(quantize_kernel<X, Q_TILE, true>) : launch(quantize_kernel<X, Q_TILE, false>);
   else
-    hipLaunchKernelGGL((quantize_simple_kernel<X, false>), grid, dim3(128), 0, s, x, sq, sl, Q, L, codes, ld_codes,
-                       scales);
+    tr ? launch(quantize_kernel<X, Q_COLUMNS, true>) : launch(quantize_kernel<X, Q_ROWS, false>);
   return hipGetLastError();
 }
 

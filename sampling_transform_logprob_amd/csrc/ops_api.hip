@@ -170,6 +170,8 @@ stce_status stce_fp8_quantize_blocks(const void* x, int32_t dtype, int64_t R, in
                 (long long)R, (long long)C);
   if (ld < C || !extent_ok(R, ld, es))
     return fail(STCE_E_ARG, "ld=%lld must be at least C=%lld", (long long)ld, (long long)C);
+  if (ceil_div(R, 128) * ceil_div(C, 128) > INT32_MAX)
+    return fail(STCE_E_UNSUPPORTED, "R=%lld x C=%lld has too many blocks for one launch", (long long)R, (long long)C);
   const int64_t L = (flags & STCE_QUANT_TRANSPOSE) ? R : C, Q = (flags & STCE_QUANT_TRANSPOSE) ? C : R;
   if (ld_codes % 16 != 0 || ld_codes < round_up(L, 16) || !extent_ok(Q, ld_codes, 1))
     return fail(STCE_E_ARG, "ld_codes=%lld must be a multiple of 16 and at least %lld", (long long)ld_codes,
