@@ -9,28 +9,33 @@ namespace {
 
 constexpr int QB = 128;  // values per scale along the reduction
 
-// fl32(v / a), clamped to the e4m3 range: the correction step of quot_fast
-// where it is exact, the IEEE division elsewhere (the same bits).
-__device__ inline float scaled_value(float v, float a, float r, bool a_ok) {
-  const float x = __builtin_fabsf(v);
-  const float q = (a_ok && x >= 0x1p-90f && x <= 0x1p+90f) ? quot_fast(v, a, r) : v / a;
-  return fminf(fmaxf(q, -E4M3_MAX), E4M3_MAX);
-}
-
+// A block's scale a, and what its codes are formed with.  The codes need
+// fl32(v / a) exactly only where |v / a| >= 2^-11 (below, every code is a zero),
+// and |v| <= 448 a (1 + 2^-24): there the correction step of quot_fast (see
+// there) gives the correctly rounded quotient as long as ulp(v / a) ulp(a) and
+// the reciprocal stay in range, for a in [2^-92, 2^125]; a smaller a and its
+// values are first multiplied by f = 2^100, which is exact.  The largest a is
+// below 2^120.
 struct BlockScale {
-  float a, r;
-  bool ok, finite;
+  float a, af, r, f;
+  bool finite;
 };
-// From the block's largest magnitude (NaN or infinite when the block holds a
-// NaN or an infinity).
+// From the block's largest magnitude (infinite when it holds a NaN or an
+// infinity).
 __device__ inline BlockScale block_scale(float mx) {
   BlockScale b;
   b.finite = mx < __builtin_huge_valf();
   const float q = mx / E4M3_MAX;
   b.a = !b.finite ? __builtin_nanf("") : q == 0.0f ? 1.0f : q;
-  b.r = 1.0f / b.a;
-  b.ok = b.a >= 0x1p-30f && b.a <= 0x1p+30f;
+  b.f = b.a < 0x1p-92f ? 0x1p100f : 1.0f;
+  b.af = b.a * b.f;
+  b.r = 1.0f / b.af;
   return b;
+}
+// fl32(v / a) clamped to the e4m3 range, with v's sign (a zero keeps it)
+__device__ inline float scaled_value(float v, const BlockScale& b) {
+  const float q = quot_fast(__builtin_fabsf(v) * b.f, b.af, b.r);
+  return __builtin_copysignf(b.finite ? fminf(q, E4M3_MAX) : 0.0f, b.finite ? v : 1.0f);
 }
 // |v|, with every non-finite value mapped to +inf so a maximum keeps it
 __device__ inline float mag(float v) {
@@ -51,38 +56,41 @@ struct __attribute__((packed, aligned(sizeof(X)))) Eight {
 
 // A workgroup of 256 threads quantizes 128 x 128 elements of x, held in
 // registers between the maximum and the codes: thread t has columns 8 (t % 16)
-// .. + 8 of rows t / 16 + 16 i, i < 8.  One read of x, one write of codes.
+// .. + 8 of rows 8 (t / 16) .. + 8.  One read of x, one write of codes.
 //   scale per row and 128 columns (ROWS):     maximum over 16 lanes
 //   scale per column and 128 rows (COLUMNS):  over a thread's rows, 4 lanes, 4 waves
 //   scale per tile (TILE):                    over the workgroup
-// With TR the codes are written transposed, through LDS (rows of 128 + 16 bytes:
-// 16-byte reads of a column's codes), else 8 bytes a thread.
-// The codes come from the hardware's conversion to e4m3 (nearest, ties to
-// even).
+// With TR the codes are written transposed, through LDS: a thread's eight codes
+// of a column are neighbours there (rows of 128 + 8 bytes; 128-byte rows go
+// out); else 8 bytes a row and thread.  The codes come from the hardware's
+// conversion to e4m3 (nearest, ties to even).
 enum : int { Q_ROWS = 0, Q_COLUMNS = 1, Q_TILE = 2 };
 template <class X, int MODE, bool TR>
 __global__ __launch_bounds__(256) void quantize_kernel(const X* x, int64_t ld, int64_t R, int64_t C, uint8_t* codes,
                                                        int64_t ldc, float* scales) {
-  constexpr int LDT = QB + 16;
+  constexpr int LDT = QB + 8;
   __shared__ float red[MODE == Q_COLUMNS ? 4 * QB : 4];
   __shared__ __attribute__((aligned(16))) uint8_t tile[TR ? QB * LDT : 16];
   const int tid = threadIdx.x, tc = tid & 15, tr = tid >> 4;
   // (neighbouring workgroups share rows of x)
   const int64_t cbs = (C + QB - 1) / QB;
   const int64_t rb = blockIdx.x / cbs, cb = blockIdx.x - rb * cbs;
-  const int64_t c0 = cb * QB + tc * 8;
+  const int64_t c0 = cb * QB + tc * 8, r0 = rb * QB + tr * 8;
   float v[8][8];
+  if (c0 + 8 <= C) {
+    Eight<X> e[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = rb * QB + tr + 16 * i;
-    if (r < R && c0 + 8 <= C) {
-      const Eight<X> e = *(const Eight<X>*)(x + r * ld + c0);
+    for (int i = 0; i < 8; ++i)
+      if (r0 + i < R) e[i] = *(const Eight<X>*)(x + (r0 + i) * ld + c0);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[i][k] = (float)e.v[k];
-    } else {
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[i][k] = r < R && c0 + k < C ? (float)x[r * ld + c0 + k] : 0.0f;
-    }
+      for (int k = 0; k < 8; ++k) v[i][k] = r0 + i < R ? (float)e[i].v[k] : 0.0f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[i][k] = r0 + i < R && c0 + k < C ? (float)x[(r0 + i) * ld + c0 + k] : 0.0f;
   }
   auto lanes = [](float m, int from, int to) {
     for (int o = from; o < to; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
@@ -96,8 +104,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(const X* x, int64_t ld, i
 #pragma unroll
       for (int k = 0; k < 8; ++k) m = fmaxf(m, mag(v[i][k]));
       s[i] = block_scale(lanes(m, 1, 16));
-      const int64_t r = rb * QB + tr + 16 * i;
-      if (tc == 0 && r < R) scales[cb * R + r] = s[i].a;
+      if (tc == 0 && r0 + i < R) scales[cb * R + r0 + i] = s[i].a;
     }
   } else if constexpr (MODE == Q_COLUMNS) {
 #pragma unroll
@@ -130,36 +137,32 @@ __global__ __launch_bounds__(256) void quantize_kernel(const X* x, int64_t ld, i
     // (scales [blocks of the reduction][tiles of the other])
     if (tid == 0) scales[TR ? rb * cbs + cb : cb * ((R + QB - 1) / QB) + rb] = s[0].a;
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint32_t w[2] = {0u, 0u};
-#pragma unroll
-    for (int k = 0; k < 8; k += 2) {
-      float q[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const BlockScale& b = s[MODE == Q_ROWS ? i : MODE == Q_COLUMNS ? k + h : 0];
-        q[h] = b.finite ? scaled_value(v[i][k + h], b.a, b.r, b.ok) : 0.0f;
-      }
-      w[k >> 2] = encode2(q[0], q[1], w[k >> 2], k & 2);
-    }
-    const int row = tr + 16 * i;
-    if constexpr (TR) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) tile[(tc * 8 + k) * LDT + row] = (uint8_t)(w[k >> 2] >> (8 * (k & 3)));
-    } else {
-      const int64_t r = rb * QB + row;
-      if (r < R && c0 < (C + 15) / 16 * 16) *(u32x2*)(codes + r * ldc + c0) = u32x2{w[0], w[1]};
-    }
-  }
+  auto code = [&](int i, int k) __attribute__((always_inline)) {
+    return scaled_value(v[i][k], s[MODE == Q_ROWS ? i : MODE == Q_COLUMNS ? k : 0]);
+  };
   if constexpr (TR) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      uint32_t w[2] = {0u, 0u};
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) w[i >> 2] = encode2(code(i, k), code(i + 1, k), w[i >> 2], i & 2);
+      *(u32x2*)(tile + (tc * 8 + k) * LDT + tr * 8) = u32x2{w[0], w[1]};
+    }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int ch = i * 256 + tid, c = ch >> 3, r16 = (ch & 7) * 16;
       const int64_t col = cb * QB + c, row = rb * QB + r16;
-      if (col < C && row < (R + 15) / 16 * 16)
-        *(u32x4*)(codes + col * ldc + row) = *(const u32x4*)(tile + c * LDT + r16);
+      const u32x2 lo = *(const u32x2*)(tile + c * LDT + r16), hi = *(const u32x2*)(tile + c * LDT + r16 + 8);
+      if (col < C && row < (R + 15) / 16 * 16) *(u32x4*)(codes + col * ldc + row) = u32x4{lo[0], lo[1], hi[0], hi[1]};
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t w[2] = {0u, 0u};
+#pragma unroll
+      for (int k = 0; k < 8; k += 2) w[k >> 2] = encode2(code(i, k), code(i, k + 1), w[k >> 2], k & 2);
+      if (r0 + i < R && c0 < (C + 15) / 16 * 16) *(u32x2*)(codes + (r0 + i) * ldc + c0) = u32x2{w[0], w[1]};
     }
   }
 }
