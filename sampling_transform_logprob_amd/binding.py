@@ -638,11 +638,13 @@ class ScoreFunction(torch.autograd.Function):
 # ---------------------------------------------------------------------------
 def _call(fn, dev, *args):
     """fn(*args, stream) on the arrays' device, on its current stream."""
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream()))
+    # (the raw queries: a torch.cuda.Stream object costs as much as a launch)
+    i = dev.index
+    if i == torch._C._cuda_getDevice():
+        _check(fn(*args, torch._C._cuda_getCurrentRawStream(i)))
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream()))
+            _check(fn(*args, torch._C._cuda_getCurrentRawStream(i)))
 
 
 def _rows(name, x, dtypes):
@@ -661,29 +663,29 @@ def _rows(name, x, dtypes):
 
 
 def _tokens(tokens, T, dev):
-    """([T, K] int64 or None, K, whether given as [T])."""
+    """(int64 [T] or [T, K] or None, K)."""
     if tokens is None:
-        return None, 0, False
+        return None, 0
     if not isinstance(tokens, torch.Tensor) or tokens.dtype != torch.int64:
         raise TypeError("tokens must be an int64 tensor or None")
     if tokens.device != dev:
         raise ValueError(f"tokens is on {tokens.device}, expected {dev}")
     if tokens.dim() not in (1, 2) or tokens.shape[0] != T:
         raise ValueError(f"tokens must have shape [{T}] or [{T}, K], got {tuple(tokens.shape)}")
-    return tokens.contiguous(), (1 if tokens.dim() == 1 else tokens.shape[1]), tokens.dim() == 1
+    return tokens.contiguous(), (1 if tokens.dim() == 1 else tokens.shape[1])
 
 
 def _token_problem(logits, tokens, temperature, top_n, ignore_index):
     z, ld = _rows("logits", logits, VALUE_DTYPES)
     T, V = z.shape
     dev = z.device
-    tok, K, flat = _tokens(tokens, T, dev)
+    tok, K = _tokens(tokens, T, dev)
     temp = _meta("temperature", temperature, T, torch.float32, dev)
     prob = TokenProblem(T, V, VALUE_DTYPES[z.dtype], 0 if ignore_index is None else PROBLEM_IGNORE_INDEX,
                         z.data_ptr(), max(ld, V), None if temp is None else temp.data_ptr(),
                         None if tok is None else tok.data_ptr(), K, top_n,
                         0 if ignore_index is None else int(ignore_index))
-    return prob, (z, tok, temp), flat
+    return prob, (z, tok, temp)
 
 
 def token_logprobs(logits, tokens=None, temperature=None, *, top_n: int = 0, ignore_index: Optional[int] = None,
@@ -700,7 +702,7 @@ def token_logprobs(logits, tokens=None, temperature=None, *, top_n: int = 0, ign
     last token with a logit above -inf).  Masked tokens (-inf) score -inf;
     ``ignore_index`` scores 0.  ``check=False`` skips the report of invalid
     tokens and temperatures, which reads one number back from the GPU."""
-    prob, keep, flat = _token_problem(logits, tokens, temperature, top_n, ignore_index)
+    prob, keep = _token_problem(logits, tokens, temperature, top_n, ignore_index)
     T, K = prob.T, prob.K
     dev = logits.device
     L = load()
@@ -708,17 +710,21 @@ def token_logprobs(logits, tokens=None, temperature=None, *, top_n: int = 0, ign
     _check(L.stce_token_workspace_bytes(ctypes.byref(prob), ctypes.byref(nb)))
     if workspace is None and nb.value:
         workspace = torch.empty(nb.value, dtype=torch.uint8, device=dev)
-    out = dict(lse=torch.empty(T, dtype=torch.float32, device=dev),
-               entropy=torch.empty(T, dtype=torch.float32, device=dev),
-               stats=torch.empty(T, 4, dtype=torch.float32, device=dev))
+    # one allocation for the fp32 outputs: a row costs little more than its calls
+    buf = torch.empty(T * (6 + K + top_n), dtype=torch.float32, device=dev)
+    out = dict(stats=buf.as_strided((T, 4), (4, 1), 0), lse=buf.as_strided((T,), (1,), 4 * T),
+               entropy=buf.as_strided((T,), (1,), 5 * T))
+    base = buf.data_ptr()
+    ptrs = [None, base + 16 * T, base + 20 * T, None, None, base]
     if tokens is not None:
-        out["logprob"] = torch.empty(tokens.shape, dtype=torch.float32, device=dev)
+        out["logprob"] = buf.as_strided(tokens.shape, (K, 1)[-tokens.dim():], 6 * T)
+        ptrs[0] = base + 24 * T
     if top_n:
-        out["top_logprob"] = torch.empty(T, top_n, dtype=torch.float32, device=dev)
-        out["top_id"] = torch.empty(T, top_n, dtype=torch.int64, device=dev)
+        out["top_logprob"] = buf.as_strided((T, top_n), (top_n, 1), (6 + K) * T)
+        out["top_id"] = torch.empty((T, top_n), dtype=torch.int64, device=dev)
+        ptrs[3], ptrs[4] = base + (24 + 4 * K) * T, out["top_id"].data_ptr()
     status = torch.empty(1, dtype=torch.int64, device=dev) if check else None
-    o = TokenOutputs(*(out[k].data_ptr() if k in out else None
-                       for k in ("logprob", "lse", "entropy", "top_logprob", "top_id", "stats")))
+    o = TokenOutputs(*ptrs)
     _call(L.stce_token_logprobs, dev, ctypes.byref(prob), ctypes.byref(o), _ptr(status), _ptr(workspace),
           0 if workspace is None else workspace.numel())
     if check:
@@ -733,7 +739,7 @@ def token_logprobs_backward(logits, tokens, stats, grad_logprob=None, grad_entro
     + sum(grad_lse * lse)`` with respect to the logits, in their dtype; ``stats``
     is the forward's.  ``grad_logits`` gives the result's place (strided rows
     allowed; not overlapping the logits)."""
-    prob, keep, flat = _token_problem(logits, tokens, temperature, 0, ignore_index)
+    prob, keep = _token_problem(logits, tokens, temperature, 0, ignore_index)
     T, V, K = prob.T, prob.V, prob.K
     dev = logits.device
     if stats.shape != (T, 4) or stats.dtype != torch.float32 or stats.device != dev or not stats.is_contiguous():

@@ -238,6 +238,7 @@ struct SegmentPlan {
   int tpc;             // tiles per cell (see below)
 };
 
+constexpr int ROWS_FILL = 512;  // rows from which every row is one workgroup's
 constexpr int CELLS = 16;      // cells of a thread at most
 constexpr int CELL_CAP = 512;  // cells that may hold alternatives
 
@@ -389,21 +390,42 @@ __global__ __launch_bounds__(TW) void token_segment_kernel(const Z* logits, int6
 }
 
 constexpr int JOIN_CAP = 1024;  // alternatives of a row's segments together
+constexpr int SEGS_MAX = 128;   // segments of a row
 
-// One wave per row: its segments' partial statistics and alternatives joined.
+// One workgroup per row: its segments' partial statistics and alternatives
+// joined.  The segments' lists are sorted, so the n-th largest of the first
+// ceil(n / segs) of each bounds the n-th largest from below; the entries that
+// reach it (at most JOIN_CAP: there are no more) are ranked.
 template <class Z, bool TOP>
-__global__ __launch_bounds__(64) void token_join_kernel(const Z* logits, int64_t ld, const float* temperature,
+__global__ __launch_bounds__(TW) void token_join_kernel(const Z* logits, int64_t ld, const float* temperature,
                                                         RowOut r, int segs, const Partial* part,
                                                         const uint64_t* tops) {
-  __shared__ uint64_t list[TOP ? JOIN_CAP : 1];
-  __shared__ uint64_t sorted[TOP_MAX];
+  __shared__ TopScratch top;
   const int64_t t = blockIdx.x;
-  const int lane = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int n = r.top_n, total = segs * n;
+  uint32_t key[4];  // of the lists' heads
+  uint64_t v[JOIN_CAP / TW];
+  if constexpr (TOP) {
+    const uint64_t* const row = tops + (size_t)t * total;
+    const int heads = (n + segs - 1) / segs * segs;  // < n + segs <= 256
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = q * 64 + lane;
+      key[q] = i < heads ? comp_key(row[(size_t)(i % segs) * n + i / segs]) : 0;
+    }
+#pragma unroll
+    for (int q = 0; q < JOIN_CAP / TW; ++q) v[q] = q * TW + tid < total ? row[q * TW + tid] : 0;
+    if (tid == 0) top.count = 0;
+  }
   const float temp = temperature ? temperature[t] : 1.0f;
   const float c = inv_temperature(temp);
+  // (every wave joins the statistics by itself, in the same order)
   float m = NEG_INF, S = 0.0f, Es = 0.0f;
-  for (int s = lane; s < segs; s += 64) {
-    const Partial p = part[t * segs + s];
+#pragma unroll
+  for (int q = 0; q < SEGS_MAX / 64; ++q) {
+    const int s = q * 64 + lane;
+    const Partial p = s < segs ? part[t * segs + s] : Partial{NEG_INF, 0.0f, 0.0f, 0.0f};
     float pm = p.m, pS = p.S, pE = p.E;
     const float mn = fmaxf(m, pm);
     rebase(m, S, Es, mn, c);
@@ -419,53 +441,36 @@ __global__ __launch_bounds__(64) void token_join_kernel(const Z* logits, int64_t
     Es += __shfl_xor(Es, o);
   }
   if constexpr (TOP) {
-    const int n = r.top_n, total = segs * n;  // <= JOIN_CAP
-    uint64_t v[JOIN_CAP / 64];
-    uint32_t key[JOIN_CAP / 64];
-#pragma unroll
-    for (int q = 0; q < JOIN_CAP / 64; ++q) {
-      v[q] = q * 64 + lane < total ? tops[(size_t)t * total + q * 64 + lane] : 0;
-      key[q] = comp_key(v[q]);
-    }
     uint32_t bar = nth_key<KeyShift<Z>::SHIFT>(key, n);
     bar = bar < KEY_LOWEST ? KEY_LOWEST : bar;
-    int cnt = 0;
+    __syncthreads();
 #pragma unroll
-    for (int q = 0; q < JOIN_CAP / 64; ++q) {
-      const uint64_t hit = __ballot(key[q] >= bar);
-      if (key[q] >= bar) list[cnt + __popcll(hit & ((1ull << lane) - 1))] = v[q];
-      cnt += __popcll(hit);
-    }
+    for (int q = 0; q < JOIN_CAP / TW; ++q)
+      if (comp_key(v[q]) >= bar) top.list[atomicAdd(&top.count, 1)] = v[q];
     __syncthreads();
-    for (int i = lane; i < n; i += 64)
-      if (i >= cnt) sorted[i] = 0;
-    for (int i = lane; i < cnt; i += 64) {
-      const uint64_t mine = list[i];
-      int rank = 0;
-      for (int j = 0; j < cnt; ++j) rank += list[j] > mine ? 1 : 0;
-      if (rank < n) sorted[rank] = mine;
-    }
-    __syncthreads();
+    rank_list(top, n);
   }
-  write_row(r, logits + t * ld, t, temp, m, S, Es, sorted, lane, 64);
+  write_row(r, logits + t * ld, t, temp, m, S, Es, top.sorted, tid, TW);
 }
 
-// How rows are cut: tiles of 8,192 elements where the rows fill the chip, of
-// 2,048 elsewhere (a short row's latency is its loads' and the lists'); about
-// 1,024 workgroups in all, as long as a row's segments' alternatives fit the
-// joining wave.
+// How rows are cut.  Rows that fill the chip by themselves take one workgroup
+// each, tiles of 8,192 elements.  Fewer rows are cut into segments, about 1,024
+// workgroups in all (as many as leave a row's segments' alternatives to one
+// joining workgroup), with the smallest tile that makes a segment one tile: all
+// its loads are then in flight at once.
 struct TokenPlan {
-  bool wide;
+  int ept;  // elements a thread and tile
   SegmentPlan s;
 };
 TokenPlan plan_tokens(const stce_token_problem& p) {
   TokenPlan t{};
-  t.wide = p.T * ceil_div(p.V, 8192) >= 1024;
-  const int64_t tiles = ceil_div(p.V, t.wide ? 8192 : 2048);
-  int64_t segs = ceil_div(1024, p.T);
-  if (segs > tiles) segs = tiles;
-  if (p.top_n && segs > JOIN_CAP / p.top_n) segs = JOIN_CAP / p.top_n;
-  const int64_t tps = ceil_div(tiles, segs);
+  int64_t most = p.T >= ROWS_FILL ? 1 : ceil_div(1024, p.T);
+  if (most > SEGS_MAX) most = SEGS_MAX;
+  if (p.top_n && most > JOIN_CAP / p.top_n) most = JOIN_CAP / p.top_n;
+  t.ept = ceil_div(p.V, 2048) <= most ? 8 : ceil_div(p.V, 4096) <= most ? 16 : 32;
+  const int64_t tiles = ceil_div(p.V, TW * t.ept);
+  if (most > tiles) most = tiles;
+  const int64_t tps = ceil_div(tiles, most);
   t.s.segs = (int)ceil_div(tiles, tps);
   t.s.tiles = (int)tiles;
   t.s.tps = (int)tps;
@@ -593,15 +598,17 @@ hipError_t run_forward_as(const stce_token_problem& p, const RowOut& r, void* ws
   uint64_t* tops = part ? (uint64_t*)(part + p.T * pl.s.segs) : nullptr;
   {
     ProfScope ps(KIND_TOKEN_LOGPROBS, s);
-    if (pl.wide)
+    if (pl.ept == 32)
       launch_segments<Z, 32, TOP>(pl, p, r, part, tops, s);
+    else if (pl.ept == 16)
+      launch_segments<Z, 16, TOP>(pl, p, r, part, tops, s);
     else
       launch_segments<Z, 8, TOP>(pl, p, r, part, tops, s);
   }
   hipError_t e = hipGetLastError();
   if (e || !part) return e;
   ProfScope ps(KIND_TOKEN_MERGE, s);
-  hipLaunchKernelGGL((token_join_kernel<Z, TOP>), dim3((unsigned)p.T), dim3(64), 0, s, (const Z*)p.logits, p.ld,
+  hipLaunchKernelGGL((token_join_kernel<Z, TOP>), dim3((unsigned)p.T), dim3(TW), 0, s, (const Z*)p.logits, p.ld,
                      p.temperature, r, pl.s.segs, part, tops);
   return hipGetLastError();
 }
