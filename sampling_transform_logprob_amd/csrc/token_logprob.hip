@@ -483,11 +483,10 @@ TokenPlan plan_tokens(const stce_token_problem& p) {
 // a1 = ln 2 grad_entropy.  One read and one write of the row, 16 bytes a
 // thread at a time; a workgroup takes `tiles` tiles of 4 granules a thread.
 //
-// A given token's gradient is added by the thread that holds its element, before
-// the one rounding: the granules that hold given tokens are marked first (one bit
-// a granule, tiles x 4 <= 32 of a thread), and a marked granule's thread looks
-// through the row's tokens in order, so a token given twice gets both and equal
-// calls give equal bits.
+// A given token's element is written once more, after a barrier, by the thread of
+// its first occurrence: with the sum of the gradients of all its occurrences, in
+// order, added before the one rounding.  So a token given twice gets both, and
+// equal calls give equal bits.
 constexpr int GRAD_NG = 4, GRAD_TILES = 8;  // granules a thread and tile; tiles a workgroup at most
 
 template <class Z, bool FEW>
@@ -499,10 +498,12 @@ __global__ __launch_bounds__(TW) void token_grad_kernel(const Z* logits, int64_t
   constexpr int E = Granule<Z>::E, TILE = TW * E * GRAD_NG;
   constexpr int CAP = FEW ? 8 : TOKENS_MAX;
   typedef typename Granule<Z>::Raw Raw;
+  typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
   __shared__ float red[TW / 64];
-  __shared__ uint32_t mark[TW];
-  __shared__ int32_t tok[CAP];
-  __shared__ float tg[CAP];
+  __shared__ i32x4 tok4[CAP / 4];
+  __shared__ f32x4 tg4[CAP / 4];
+  int32_t* const tok = (int32_t*)tok4;
+  float* const tg = (float*)tg4;
   const int tid = threadIdx.x;
   const int64_t t = blockIdx.x / segs;
   const int64_t j0 = (int64_t)(blockIdx.x - (int)t * segs) * tiles * TILE;
@@ -515,35 +516,24 @@ __global__ __launch_bounds__(TW) void token_grad_kernel(const Z* logits, int64_t
       bad_temperature(temp) || !(st.m > NEG_INF && st.m < __builtin_huge_valf()) || st.log_sum != st.log_sum;
   const float c = inv_temperature(temp), l2 = st.log_sum * LOG2E;
   const float rt = fminf(1.0f / temp, 3.4028235e38f);
-  mark[tid] = 0;
-  __syncthreads();
   float g = 0.0f;
+  const int K4 = (K + 3) & ~3;
   if (g_lp) {
-    for (int i = tid; i < K; i += TW) {
-      const int64_t y = tokens[t * K + i];
+    for (int i = tid; i < K4; i += TW) {
+      const int64_t y = i < K ? tokens[t * K + i] : -1;
       const bool ok = y >= 0 && y < V && to_f32(z[y]) > NEG_INF;
       const float v = ok ? g_lp[t * K + i] : 0.0f;
       tok[i] = ok ? (int32_t)y : -1;
       tg[i] = v;
       g += v;
-      if (ok && y >= j0 && y < j1) {
-        const int64_t at = y - j0, in = at % TILE;
-        atomicOr(&mark[in / E % TW], 1u << (int)(at / TILE * GRAD_NG + in / (E * TW)));
-      }
     }
-    g = block_reduce<false>(g, red);  // (its barriers make the marks and tokens visible)
+    g = block_reduce<false>(g, red);  // (its barriers make the tokens visible)
   }
   const float ge = g_ent ? g_ent[t] : 0.0f, gl = g_lse ? g_lse[t] : 0.0f;
   const float a0 = gl - g - ge * st.entropy, a1 = ge * LN2;
-  const uint32_t marks = mark[tid];
   auto one = [&](Z v) __attribute__((always_inline)) {
     const float x = fmaxf((to_f32(v) - st.m) * c - l2, -200.0f);
     return none ? 0.0f : exp2_fast(x) * __builtin_fmaf(-a1, x, a0) * rt;
-  };
-  auto given = [&](int64_t j) __attribute__((always_inline)) {
-    float v = 0.0f;
-    for (int i = 0; i < K; ++i) v += tok[i] == (int32_t)j ? tg[i] : 0.0f;
-    return none ? 0.0f : v * rt;
   };
   for (int tile = 0; tile < tiles; ++tile) {
     const int64_t b = j0 + (int64_t)tile * TILE + tid * E;
@@ -554,27 +544,47 @@ __global__ __launch_bounds__(TW) void token_grad_kernel(const Z* logits, int64_t
       for (int q = 0; q < GRAD_NG; ++q) in[q] = *(const Raw*)(z + b + q * TW * E);
 #pragma unroll
       for (int q = 0; q < GRAD_NG; ++q) {
-        float d[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) d[e] = one(in[q].v[e]);
-        if (marks >> (tile * GRAD_NG + q) & 1) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) d[e] += given(b + q * TW * E + e);
-        }
         Raw o;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o.v[e] = (Z)d[e];
+        for (int e = 0; e < E; ++e) o.v[e] = (Z)one(in[q].v[e]);
         *(Raw*)(dz + b + q * TW * E) = o;
       }
     } else {
+#pragma unroll
       for (int q = 0; q < GRAD_NG; ++q) {
-        const bool marked = marks >> (tile * GRAD_NG + q) & 1;
-        for (int e = 0; e < E; ++e) {
-          const int64_t j = b + q * TW * E + e;
-          if (j < V) dz[j] = (Z)(one(z[j]) + (marked ? given(j) : 0.0f));
+        const int64_t j = b + q * TW * E;
+        if (j + E <= V) {
+          const Raw in = *(const Raw*)(z + j);
+          Raw o;
+#pragma unroll
+          for (int e = 0; e < E; ++e) o.v[e] = (Z)one(in.v[e]);
+          *(Raw*)(dz + j) = o;
+        } else {
+          for (int e = 0; e < E; ++e)
+            if (j + e < V) dz[j + e] = (Z)one(z[j + e]);
         }
       }
     }
+  }
+  if (!g_lp || none) return;
+  __syncthreads();  // the elements written again below were written above by other threads
+  for (int i = tid; i < K; i += TW) {
+    const int32_t y = tok[i];
+    if (y < j0 || y >= j1) continue;
+    bool first = true;
+    float v = 0.0f;
+    for (int k = 0; k < K4; k += 4) {
+      const i32x4 o = tok4[k / 4];
+      const f32x4 w = tg4[k / 4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (o[e] == y) {
+          v += w[e];
+          first = first && k + e >= i;
+        }
+      }
+    }
+    if (first) dz[y] = (Z)(one(z[y]) + v * rt);
   }
 }
 
