@@ -218,11 +218,11 @@ struct BlockOut {
   int add;
 };
 
-// 256 rows of b by 64 NJ rows of a per workgroup; segment g of the reduction
+// 128 WB rows of b by 64 NJ rows of a per workgroup; segment g of the reduction
 // (blocks [g per, (g + 1) per)) goes to its own partial output.
-template <int NJ, bool ROWB, class F, class O>
-__global__ __launch_bounds__(512, 1) void block_tile_kernel(BlockOps p, BlockOut o, TileMap map, int per) {
-  using Main = BlockMain<NJ, ROWB, F>;
+template <int NJ, bool ROWB, class F, int WB, class O>
+__global__ __launch_bounds__(256 * WB, 3 - WB) void block_tile_kernel(BlockOps p, BlockOut o, TileMap map, int per) {
+  using Main = BlockMain<NJ, ROWB, F, WB>;
   const int tiles = map.tiles_m * map.tiles_n;
   const int g = blockIdx.x / tiles;
   int tn, tm;
@@ -246,104 +246,6 @@ __global__ __launch_bounds__(512, 1) void block_tile_kernel(BlockOps p, BlockOut
   }
 }
 
-// Few rows of a (at most 16 TG): bound by b's bytes, which go from memory to
-// registers without LDS (no wave shares them).  A workgroup of four waves
-// forms 16 RG rows of b by all rows of a; the waves take the reduction's blocks
-// in turn (neighbouring 128-byte pieces of the same rows) and their sums are
-// added in wave order.  Every product is exact: fp16 matrix instructions, whose
-// rate does not matter here.
-template <int RG, int TG, bool ROWB, class O>
-__global__ __launch_bounds__(256) void block_skinny_kernel(BlockOps p, BlockOut o, int per) {
-  __shared__ f32x4 sums[4][RG * TG][64];
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int row = lane & 15, q = lane >> 4;
-  const int n0 = blockIdx.x * 16 * RG, g = blockIdx.y;
-  const int nkb = (p.K + QB - 1) / QB;
-  const int kb0 = g * per, kb1 = min(kb0 + per, nkb);
-  const uint8_t* pb[RG];
-  const uint8_t* pa[TG];
-  const float* psa[TG];
-#pragma unroll
-  for (int i = 0; i < RG; ++i) pb[i] = p.b + (int64_t)min(n0 + i * 16 + row, p.N - 1) * p.ldb + q * 16;
-#pragma unroll
-  for (int j = 0; j < TG; ++j) {
-    const int m = min(j * 16 + row, p.M - 1);
-    pa[j] = p.a + (int64_t)m * p.lda + q * 16;
-    psa[j] = p.sa + (int64_t)m * p.sa_row;
-  }
-  struct Tile {
-    u32x4 b[RG][2], a[TG][2];
-    float sa[TG], sb[ROWB ? RG * 4 : 1];
-  };
-  auto load = [&](Tile& t, int kb) __attribute__((always_inline)) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = kb * QB + h * 64;
-      const bool in = k + q * 16 < p.K;
-#pragma unroll
-      for (int i = 0; i < RG; ++i) t.b[i][h] = in ? *(const u32x4*)(pb[i] + k) : u32x4{};
-#pragma unroll
-      for (int j = 0; j < TG; ++j) t.a[j][h] = in ? *(const u32x4*)(pa[j] + k) : u32x4{};
-    }
-#pragma unroll
-    for (int j = 0; j < TG; ++j) t.sa[j] = psa[j][kb * p.sa_blk];
-    if constexpr (ROWB) {
-#pragma unroll
-      for (int i = 0; i < RG; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          t.sb[i * 4 + r] = p.sb[(int64_t)min(n0 + i * 16 + q * 4 + r, p.N - 1) * p.sb_row + kb * p.sb_blk];
-    } else {
-      t.sb[0] = p.sb[(int64_t)(n0 / QB) * p.sb_row + kb * p.sb_blk];  // (16 RG rows lie in one tile)
-    }
-  };
-  f32x4 acc[RG][TG];
-#pragma unroll
-  for (int i = 0; i < RG; ++i)
-#pragma unroll
-    for (int j = 0; j < TG; ++j) acc[i][j] = f32x4{};
-  auto mul = [&](const Tile& t) __attribute__((always_inline)) {
-    FragF16 fa[TG];
-#pragma unroll
-    for (int j = 0; j < TG; ++j) fa[j] = FragF16(raw_frag(t.a[j][0], t.a[j][1]));
-#pragma unroll
-    for (int i = 0; i < RG; ++i) {
-      const FragF16 fb(raw_frag(t.b[i][0], t.b[i][1]));
-#pragma unroll
-      for (int j = 0; j < TG; ++j) {
-        const f32x4 part = block_mfma(fb, fa[j]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[i][j][r] = __builtin_fmaf(part[r], t.sa[j] * t.sb[ROWB ? i * 4 + r : 0], acc[i][j][r]);
-      }
-    }
-  };
-  Tile t[2];
-  int kb = kb0 + w;
-  if (kb < kb1) load(t[0], kb);
-  for (; kb < kb1; kb += 8) {
-    if (kb + 4 < kb1) load(t[1], kb + 4);
-    mul(t[0]);
-    if (kb + 4 < kb1) {
-      if (kb + 8 < kb1) load(t[0], kb + 8);
-      mul(t[1]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < RG; ++i)
-#pragma unroll
-    for (int j = 0; j < TG; ++j) sums[w][i * TG + j][lane] = acc[i][j];
-  __syncthreads();
-  O* const out = (O*)o.out + g * o.split;
-  for (int s = w; s < RG * TG; s += 4) {
-    f32x4 v = sums[0][s][lane];
-#pragma unroll
-    for (int x = 1; x < 4; ++x) v += sums[x][s][lane];
-    const int m = (s % TG) * 16 + row, n = n0 + (s / TG) * 16 + q * 4;
-    if (m < p.M && n < p.N) store4(out + (int64_t)m * o.ldo + n, v, p.N - n, o.add);
-  }
-}
-
 // out (+)= the segments' partial results [S][M][N], added in order.
 template <class O>
 __global__ __launch_bounds__(256) void block_sum_kernel(const float* part, int S, int64_t M, int64_t N, O* out,
@@ -363,63 +265,40 @@ __global__ __launch_bounds__(256) void block_zero_kernel(int64_t M, int64_t N, O
     out[e / N * ldo + e % N] = (O)0.0f;
 }
 
-// How a product is cut: rows of a up to 64 take the skinny kernel.  Segments of
-// the reduction fill the chip when there are few output tiles.
+// How a product is cut.  Large 16-bit outputs with tile scales take 256 x 256
+// tiles of eight waves (NJ = 4, the fewest operand bytes per product);
+// everything else four waves and 128 rows of b by 128 rows of a, or by 64 when
+// there are no more: two or three such workgroups share a compute unit and cover
+// each other's barriers.  Small M is bound by b's bytes, which those keep in
+// flight (5.8 TB/s of 151,936 x 5,120 codes for one row of a).  Segments of the
+// reduction fill the chip when there are few output tiles.
 struct BlockPlan {
-  bool skinny;
-  int rg, tg, nj;      // skinny: 16-row groups of b and of a; tiled: NJ
+  int nj;
   int64_t tiles_n, tiles_m;
-  int S, per;          // segments, blocks per segment
+  int S, per;  // segments, blocks per segment
 };
 
 BlockPlan plan_product(const stce_block_matmul& p) {
   BlockPlan b{};
   const int64_t nkb = ceil_div(p.K, QB);
-  int64_t wgs, want, least;  // workgroups of one segment, wanted in all, blocks a segment has at least
-  b.skinny = p.M <= 64;
-  if (b.skinny) {
-    b.rg = ceil_div(p.N, 64) >= 384 ? 4 : 1;
-    b.tg = p.M <= 16 ? 1 : p.M <= 32 ? 2 : 4;
-    b.tiles_n = ceil_div(p.N, 16 * b.rg);
-    wgs = b.tiles_n;
-    want = 512;
-    least = 4;
-  } else {
-    b.nj = p.M > 128 && p.out_dtype != STCE_DT_F32 && p.b_rows == QB ? 4 : 2;
-    b.tiles_n = ceil_div(p.N, 256);
-    b.tiles_m = ceil_div(p.M, 64 * b.nj);
-    wgs = b.tiles_n * b.tiles_m;
-    want = 256;
-    least = 4;
-  }
-  int64_t S = wgs >= want ? 1 : want / wgs;
-  if (S > ceil_div(nkb, least)) S = ceil_div(nkb, least);
+  b.nj = p.M <= 64 ? 1 : p.M > 128 && p.out_dtype != STCE_DT_F32 && p.b_rows == QB ? 4 : 2;
+  b.tiles_n = ceil_div(p.N, b.nj == 4 ? 256 : 128);
+  b.tiles_m = ceil_div(p.M, 64 * b.nj);
+  const int64_t wgs = b.tiles_n * b.tiles_m;
+  int64_t S = 256 / wgs;  // (compute units; at least four blocks a segment)
+  if (S > ceil_div(nkb, 4)) S = ceil_div(nkb, 4);
   if (S < 1) S = 1;
   b.per = (int)ceil_div(nkb, S);
   b.S = nkb ? (int)ceil_div(nkb, b.per) : 1;
   return b;
 }
 
-template <bool ROWB, class O>
-void launch_skinny(const BlockPlan& b, const BlockOps& p, const BlockOut& o, hipStream_t s) {
-  const dim3 grid((unsigned)b.tiles_n, (unsigned)b.S);
-#define STCE_SKINNY(RG, TG) \
-  if (b.rg == RG && b.tg == TG) \
-  hipLaunchKernelGGL((block_skinny_kernel<RG, TG, ROWB, O>), grid, dim3(256), 0, s, p, o, b.per)
-  STCE_SKINNY(1, 1);
-  STCE_SKINNY(1, 2);
-  STCE_SKINNY(1, 4);
-  STCE_SKINNY(4, 1);
-  STCE_SKINNY(4, 2);
-  STCE_SKINNY(4, 4);
-#undef STCE_SKINNY
-}
-
 template <int NJ, bool ROWB, class F, class O>
 void launch_tiles(const BlockPlan& b, const BlockOps& p, const BlockOut& o, hipStream_t s) {
+  constexpr int WB = NJ == 4 ? 2 : 1;
   const TileMap map{(int)b.tiles_n, (int)b.tiles_m, 4};
-  hipLaunchKernelGGL((block_tile_kernel<NJ, ROWB, F, O>), dim3((unsigned)(b.tiles_n * b.tiles_m * b.S)), dim3(512), 0,
-                     s, p, o, map, b.per);
+  hipLaunchKernelGGL((block_tile_kernel<NJ, ROWB, F, WB, O>), dim3((unsigned)(b.tiles_n * b.tiles_m * b.S)),
+                     dim3(256 * WB), 0, s, p, o, map, b.per);
 }
 
 // A 16-bit output is rounded far above what the fp8 matrix instructions drop
@@ -427,23 +306,21 @@ void launch_tiles(const BlockPlan& b, const BlockOps& p, const BlockOut& o, hipS
 // and keep 13 binary places below it: 1.5e-5 of a 128-term sum of normal
 // values); an fp32 output takes the fp16 ones on converted codes, exact
 // products summed to 9e-9, at half the rate.
-template <bool ROWB, class O, bool EXACT>
+template <bool ROWB, class O, class F>
 void launch_product(const BlockPlan& b, const BlockOps& p, const BlockOut& o, hipStream_t s) {
-  if (b.skinny) return launch_skinny<ROWB, O>(b, p, o, s);
-  if constexpr (EXACT) {
-    launch_tiles<2, ROWB, FragF16, O>(b, p, o, s);
-  } else {
-    if constexpr (!ROWB)
-      if (b.nj == 4) return launch_tiles<4, ROWB, FragFp8, O>(b, p, o, s);
-    launch_tiles<2, ROWB, FragFp8, O>(b, p, o, s);
-  }
+  if constexpr (!ROWB && std::is_same<F, FragFp8>::value)
+    if (b.nj == 4) return launch_tiles<4, ROWB, F, O>(b, p, o, s);
+  if (b.nj == 1)
+    launch_tiles<1, ROWB, F, O>(b, p, o, s);
+  else
+    launch_tiles<2, ROWB, F, O>(b, p, o, s);
 }
 
 unsigned sweep_blocks(int64_t n) { return (unsigned)(ceil_div(n, 256) < 8192 ? ceil_div(n, 256) : 8192); }
 
 template <class O>
 hipError_t run_matmul(const stce_block_matmul& p, void* ws, hipStream_t s) {
-  constexpr bool EXACT = sizeof(O) == 4;
+  using F = typename std::conditional<sizeof(O) == 4, FragF16, FragFp8>::type;
   ProfScope ps(KIND_BLOCK_MATMUL, s);
   if (p.K == 0) {
     if (!p.accumulate)
@@ -459,16 +336,16 @@ hipError_t run_matmul(const stce_block_matmul& p, void* ws, hipStream_t s) {
   if (b.S == 1) {
     const BlockOut o{p.out, p.ldo, 0, p.accumulate};
     if (rowb)
-      launch_product<true, O, EXACT>(b, ops, o, s);
+      launch_product<true, O, F>(b, ops, o, s);
     else
-      launch_product<false, O, EXACT>(b, ops, o, s);
+      launch_product<false, O, F>(b, ops, o, s);
     return hipGetLastError();
   }
   const BlockOut o{ws, p.N, p.M * p.N, 0};
   if (rowb)
-    launch_product<true, float, EXACT>(b, ops, o, s);
+    launch_product<true, float, F>(b, ops, o, s);
   else
-    launch_product<false, float, EXACT>(b, ops, o, s);
+    launch_product<false, float, F>(b, ops, o, s);
   const hipError_t e = hipGetLastError();
   if (e) return e;
   hipLaunchKernelGGL(block_sum_kernel<O>, dim3(sweep_blocks(p.M * p.N)), dim3(256), 0, s, (const float*)ws, b.S, p.M,

@@ -2,13 +2,13 @@
 // the reduction (gfx950): out[m, n] = sum_b sa[m, b] sb[n, b] P_b[m, n], P_b the
 // sum over the 128 k of block b.
 //
-// A workgroup (512 threads, 8 waves) forms 256 rows n of b by 64 NJ rows m of
-// a; the waves lie 2 (n) x 4 (m), each 128 x 16 NJ outputs as 8 x NJ blocks of
+// A workgroup of 4 WB waves forms 128 WB rows n of b by 64 NJ rows m of a; the
+// waves lie WB (n) x 4 (m), each 128 x 16 NJ outputs as 8 x NJ blocks of
 // 16 x 16, with b as the first matrix operand: a lane then holds one row m and
 // four consecutive n, so a per-tile scale of b is one value per wave, and an
 // output store four neighbours.  A k-tile is one scale block, 128 bytes of a
 // row; the loads, the LDS layout and its swizzle are those of the fp8 loop in
-// gemm.hpp, plus 1 KB of scales for each operand (one dword per row).
+// gemm.hpp, plus the scales (one dword per row).
 //
 // A matrix instruction of k-tile t starts from zero; its four results are
 // scaled into the running fp32 sums by ordinary fma, one row of blocks behind
@@ -64,7 +64,7 @@ __device__ inline f32x4 block_mfma(const FragF16& a, const FragF16& b) {
   return p;
 }
 
-// Operands of the tiled and the skinny kernels.
+// Operands of the product.
 struct BlockOps {
   const uint8_t* a;
   const uint8_t* b;
@@ -77,29 +77,28 @@ struct BlockOps {
 };
 
 // NJ: 16-row blocks of a per wave.  ROWB: one scale per row of b (else per 128).
-// F: the fragment type, FragFp8 or FragF16.
-template <int NJ, bool ROWB, class F>
+// F: the fragment type, FragFp8 or FragF16.  WB: waves along n (4 WB in all).
+template <int NJ, bool ROWB, class F, int WB>
 struct BlockMain {
-  static constexpr int TN = 256, TM = 64 * NJ;  // rows of b, of a per workgroup
-  static constexpr int LB = 4, LA = NJ;          // 1 KB loads per wave, operand and k-tile
+  static constexpr int THREADS = 256 * WB;
+  static constexpr int TN = 128 * WB, TM = 64 * NJ;  // rows of b, of a per workgroup
+  static_assert(TM <= TN, "the scales of a take as many loads as those of b");
+  static constexpr int LB = 4, LA = 2 * NJ / WB;  // 1 KB loads per wave, operand and k-tile
   static constexpr int BYTES_B = TN * 128, BYTES_A = TM * 128;
-  static constexpr int STAGE = BYTES_B + BYTES_A + 2048;  // + scales of b (1 KB) and of a (1 KB)
-  static constexpr int OFF_A = BYTES_B, OFF_SB = BYTES_B + BYTES_A, OFF_SA = OFF_SB + 1024;
+  static constexpr int STAGE = BYTES_B + BYTES_A + 8 * TN;  // + TN scales each of b and of a
+  static constexpr int OFF_A = BYTES_B, OFF_SB = BYTES_B + BYTES_A, OFF_SA = OFF_SB + 4 * TN;
   typedef f32x4 Acc[8][NJ];
 
-  __device__ static char* stage0() {
-    __shared__ __attribute__((aligned(16))) char s0[STAGE];
-    return s0;
-  }
-  __device__ static char* stage1() {
-    __shared__ __attribute__((aligned(16))) char s1[STAGE];
-    return s1;
+  // each stage an object of its own: the compiler then knows that the loads in
+  // flight into one do not touch the others
+  template <int I>
+  __device__ static char* stage() {
+    __shared__ __attribute__((aligned(16))) char s[STAGE];
+    return s;
   }
 
   // k-tiles kt0 .. kt1 (kt0 < kt1) of the output tile at (n0, m0)
   __device__ static inline void run(const BlockOps& p, Acc& acc, int n0, int m0, int kt0, int kt1) {
-    char* const S0 = stage0();
-    char* const S1 = stage1();
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wb = w >> 2, wa = w & 3;
@@ -114,17 +113,17 @@ struct BlockMain {
     const int lrow = lane >> 3, lpc = lane & 7;
     const int ce = lpc ^ lds_swz(lrow), co = lpc ^ lds_swz(lrow + 8);
     const int rB = (w * LB * 8 + lrow) * ldb, rA = (w * LA * 8 + lrow) * lda;
-    // scales: wave w < 4 loads rows 64 w .. of b's, the others of a's
-    const bool isb = w < 4;
-    const int srow = (w & 3) * 64 + lane;
+    // scales: the first half of the waves loads 64 rows each of b's, the others of a's
+    const bool isb = w < 2 * WB;
+    const int sw0 = (w & (2 * WB - 1)) * 64, srow = sw0 + lane;
     const int nbase = ROWB ? n0 : n0 >> 7;
     const int soff = isb ? ((ROWB ? min(n0 + srow, p.N - 1) : min(n0 + srow, p.N - 1) >> 7) - nbase) * p.sb_row * 4
                          : min(srow, rowsA - 1) * p.sa_row * 4;
     const float* const sbase = isb ? p.sb + (int64_t)nbase * p.sb_row : p.sa + (int64_t)m0 * p.sa_row;
     const int64_t sblk = isb ? p.sb_blk : p.sa_blk;
-    const int lds_s = (isb ? OFF_SB : OFF_SA) + (w & 3) * 256;
-    auto issue = [&](int sg, int kt) __attribute__((always_inline)) {
-      char* const st = sg ? S1 : S0;
+    const int lds_s = (isb ? OFF_SB : OFF_SA) + sw0 * 4;
+    auto issue = [&](auto sg_c, int kt) __attribute__((always_inline)) {
+      char* const st = stage<decltype(sg_c)::value>();
       const int k0 = kt * 128;
       const int kend = min(p.K, kt1 * 128);
       const bool ine = k0 + ce * 16 < kend, ino = k0 + co * 16 < kend;
@@ -208,20 +207,20 @@ struct BlockMain {
     };
     auto tile = [&](auto sg_c, int kt) __attribute__((always_inline)) {
       constexpr int sg = decltype(sg_c)::value;
-      const char* const st = sg ? S1 : S0;
-      const char* const nx = sg ? S0 : S1;
+      const char* const st = stage<sg>();
+      const char* const nx = stage<1 - sg>();
       F cb;
 #pragma unroll
       for (int idx = 0; idx < NM; ++idx) {
         const int i = idx / NJ, j = idx % NJ;
         if (j == 0) {
           if (i == 8 - AHEAD) {
-            // every wave has read all of stage sg, and the next tile has landed
+            // every wave has read all of this stage, and the next tile has landed
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_waitcnt(WAIT_VM0_LGKM0);
             __syncthreads();
             __builtin_amdgcn_sched_barrier(0);
-            issue(sg, kt + 2);
+            issue(sg_c, kt + 2);
             read_scales(nx, 1 - sg, kt + 1 < kt1);
           }
           if (i + AHEAD < 8)
@@ -239,26 +238,27 @@ struct BlockMain {
       }
       __builtin_amdgcn_sched_barrier(0);
     };
-    issue(0, kt0);
-    issue(1, kt0 + 1);
+    // Tiles run in pairs, so that stages and slots are constants; an odd count
+    // gets one more tile of zeros (its loads fall past the end, its scales are
+    // zero).
+    constexpr std::integral_constant<int, 0> S0{};
+    constexpr std::integral_constant<int, 1> S1{};
+    issue(S0, kt0);
+    issue(S1, kt0 + 1);
     __builtin_amdgcn_s_waitcnt(WAIT_VM0_LGKM0);
     __syncthreads();
-    read_scales(S0, 0, true);
+    read_scales(stage<0>(), 0, true);
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) read_b(S0, i, true);
+    for (int i = 0; i < AHEAD; ++i) read_b(stage<0>(), i, true);
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) fa[j] = frag(S0 + offA + j * 16 * 128);
-    const int nk2 = (kt1 - kt0 + 1) & ~1;
-    using Z_ = std::integral_constant<int, 0>;
-    using O_ = std::integral_constant<int, 1>;
-    for (int kt = kt0; kt < kt0 + nk2; kt += 2) {
-      tile(Z_{}, kt);
-      tile(O_{}, kt + 1);
+    for (int j = 0; j < NJ; ++j) fa[j] = frag(stage<0>() + offA + j * 16 * 128);
+    for (int kt = kt0; kt < kt1; kt += 2) {
+      tile(S0, kt);
+      tile(S1, kt + 1);
     }
 #pragma unroll
     for (int idx = NM - LAG; idx < NM; ++idx) scale_in(idx, 1);
-    __builtin_amdgcn_s_waitcnt(WAIT_VM0_LGKM0);
-    __syncthreads();
+    __builtin_amdgcn_s_waitcnt(WAIT_VM0_LGKM0);  // (no load may land after the workgroup has gone)
   }
 };
 

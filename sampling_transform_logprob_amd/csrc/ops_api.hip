@@ -98,8 +98,8 @@ stce_status check_matmul_shapes(const stce_block_matmul* p) {
   // (the rows of a tile's scales are addressed with 32-bit byte offsets)
   if (p->a_row_stride > (1 << 20) || p->b_row_stride > (1 << 20))
     return fail(STCE_E_UNSUPPORTED, "scale row strides must be at most 2^20 elements");
-  // (the launch: one workgroup per 16 x M or 256 x 64 outputs)
-  if (p->M > 64 && ceil_div(p->M, 64) * ceil_div(p->N, 256) > INT32_MAX / 2)
+  // (a workgroup forms at least 128 x 128 outputs where there are more than 64 rows)
+  if (ceil_div(p->M, 64) * ceil_div(p->N, 128) > INT32_MAX / 2)
     return fail(STCE_E_UNSUPPORTED, "M=%lld x N=%lld has too many output tiles", (long long)p->M, (long long)p->N);
   if (p->accumulate && p->out_dtype != STCE_DT_F32)
     return fail(STCE_E_UNSUPPORTED, "accumulate takes an fp32 output");
