@@ -122,32 +122,33 @@ struct BlockMain {
     const float* const sbase = isb ? p.sb + (int64_t)nbase * p.sb_row : p.sa + (int64_t)m0 * p.sa_row;
     const int64_t sblk = isb ? p.sb_blk : p.sa_blk;
     const int lds_s = (isb ? OFF_SB : OFF_SA) + sw0 * 4;
-    auto issue = [&](auto sg_c, int kt) __attribute__((always_inline)) {
+    // load x of a k-tile: LB of b, LA of a, the scales
+    constexpr int LOADS = LB + LA + 1;
+    auto issue = [&](auto sg_c, int kt, int x) __attribute__((always_inline)) {
       char* const st = stage<decltype(sg_c)::value>();
       const int k0 = kt * 128;
       const int kend = min(p.K, kt1 * 128);
-      const bool ine = k0 + ce * 16 < kend, ino = k0 + co * 16 < kend;
-      // (eight rows on: formed anew for every load, or the lane offsets of all
+      // (the row step is formed anew for every load, or the lane offsets of all
       // of them would stay in registers)
-      int stepB = 8 * ldb, stepA = 8 * lda;
-      asm volatile("" : "+s"(stepB), "+s"(stepA));
-#pragma unroll
-      for (int i = 0; i < LB; ++i) {
-        const bool odd = (w * LB + i) & 1;  // (the swizzle takes row bits 1 .. 3, bit 3 this parity)
-        const int c16 = (odd ? co : ce) * 16;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, STCE_LDS(st + (w * LB + i) * 1024), 16,
-                                                 (odd ? ino : ine) ? rB + c16 + i * stepB : 0x7ffffff0, k0, 0, 0);
+      if (x < LB + LA) {
+        const bool ofb = x < LB;
+        const int i = ofb ? x : x - LB, L = ofb ? LB : LA;
+        const bool odd = (w * L + i) & 1;  // (the swizzle takes row bits 1 .. 3, bit 3 this parity)
+        const int ch = odd ? co : ce;
+        int step = 8 * (ofb ? ldb : lda);
+        asm volatile("" : "+s"(step));
+        const int off = k0 + ch * 16 < kend ? (ofb ? rB : rA) + ch * 16 + i * step : 0x7ffffff0;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ofb ? rb : ra, STCE_LDS(st + (ofb ? 0 : OFF_A) + (w * L + i) * 1024), 16,
+                                                 off, k0, 0, 0);
+      } else {
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)(sbase + (int64_t)min(kt, kt1 - 1) * sblk), (short)0, 0x7fffffff, RSRC_WORD3);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, STCE_LDS(st + lds_s), 4, soff, 0, 0, 0);
       }
+    };
+    auto issue_all = [&](auto sg_c, int kt) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < LA; ++i) {
-        const bool odd = (w * LA + i) & 1;
-        const int c16 = (odd ? co : ce) * 16;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, STCE_LDS(st + OFF_A + (w * LA + i) * 1024), 16,
-                                                 (odd ? ino : ine) ? rA + c16 + i * stepA : 0x7ffffff0, k0, 0, 0);
-      }
-      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(sbase + (int64_t)min(kt, kt1 - 1) * sblk), (short)0, 0x7fffffff, RSRC_WORD3);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, STCE_LDS(st + lds_s), 4, soff, 0, 0, 0);
+      for (int x = 0; x < LOADS; ++x) issue(sg_c, kt, x);
     };
     const int frow = lane & 15, fq = lane >> 4, sw = lds_swz(frow);
     const int offB = (wb * 128 + frow) * 128, offA = OFF_A + (wa * 16 * NJ + frow) * 128;
@@ -196,12 +197,18 @@ struct BlockMain {
         for (int r = 0; r < 4; ++r) sbv[i][r] = live ? sbv[i][r] : 0.0f;
       }
     };
-    auto read_scales = [&](const char* st, int sg, bool live) __attribute__((always_inline)) {
+    // scales of a tile: read as they lie once it has landed, multiplied when it starts
+    float rsa[NJ], rsb = 1.0f;
+    auto read_scales = [&](const char* st) __attribute__((always_inline)) {
       const float* sa = (const float*)(st + OFF_SA) + wa * 16 * NJ + frow;
-      const float sb = ROWB ? 1.0f : *((const float*)(st + OFF_SB) + wb * 128);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) rsa[j] = sa[j * 16];
+      if constexpr (!ROWB) rsb = *((const float*)(st + OFF_SB) + wb * 128);
+    };
+    auto set_scales = [&](int sg, bool live) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        const float v = ROWB ? sa[j * 16] : sa[j * 16] * sb;
+        const float v = ROWB ? rsa[j] : rsa[j] * rsb;
         s[sg][j] = live ? v : 0.0f;
       }
     };
@@ -220,8 +227,6 @@ struct BlockMain {
             __builtin_amdgcn_s_waitcnt(WAIT_VM0_LGKM0);
             __syncthreads();
             __builtin_amdgcn_sched_barrier(0);
-            issue(sg_c, kt + 2);
-            read_scales(nx, 1 - sg, kt + 1 < kt1);
           }
           if (i + AHEAD < 8)
             read_b(st, i + AHEAD, kt < kt1);
@@ -233,6 +238,14 @@ struct BlockMain {
         if (idx < LAG) scale_in(NM + idx - LAG, 1 - sg);
         part[idx & 3] = block_mfma(cb, F(fa[j]));
         if (idx >= LAG) scale_in(idx - LAG, sg);
+        if (idx == 0) set_scales(sg, kt < kt1);
+        // behind the barrier: the loads of the tile after the next one into the
+        // stage just freed, a few behind every matrix instruction
+        constexpr int FIRST = (8 - AHEAD) * NJ, PER = (LOADS + NM - FIRST - 1) / (NM - FIRST);
+#pragma unroll
+        for (int x = 0; x < PER; ++x)
+          if (idx >= FIRST && (idx - FIRST) * PER + x < LOADS) issue(sg_c, kt + 2, (idx - FIRST) * PER + x);
+        if (idx == FIRST) read_scales(nx);
         if (i == 7) fa[j] = frag(nx + offA + j * 16 * 128);
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -243,11 +256,11 @@ struct BlockMain {
     // zero).
     constexpr std::integral_constant<int, 0> S0{};
     constexpr std::integral_constant<int, 1> S1{};
-    issue(S0, kt0);
-    issue(S1, kt0 + 1);
+    issue_all(S0, kt0);
+    issue_all(S1, kt0 + 1);
     __builtin_amdgcn_s_waitcnt(WAIT_VM0_LGKM0);
     __syncthreads();
-    read_scales(stage<0>(), 0, true);
+    read_scales(stage<0>());
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) read_b(stage<0>(), i, true);
 #pragma unroll
