@@ -186,30 +186,12 @@ hipError_t run_quantize(const X* x, int64_t R, int64_t C, int64_t ld, int flags,
 // ---------------------------------------------------------------------------
 // product
 // ---------------------------------------------------------------------------
-// Four neighbouring outputs of one row, n of which exist, rounded to O (added
-// to what is there with add).
+// 16 bytes of neighbouring outputs of one row.
 template <class O>
-struct __attribute__((packed, aligned(sizeof(O)))) Out4 {
-  O v[4];
+struct __attribute__((packed, aligned(sizeof(O)))) OutPiece {
+  static constexpr int E = 16 / sizeof(O);
+  O v[E];
 };
-template <class O>
-__device__ inline void store4(O* dst, f32x4 v, int n, bool add) {
-  if (n >= 4) {
-    Out4<O> o;
-    if (add) {
-      o = *(const Out4<O>*)dst;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] += (float)o.v[r];
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) o.v[r] = (O)v[r];
-    *(Out4<O>*)dst = o;
-  } else {
-#pragma unroll
-    for (int r = 0; r < 3; ++r)
-      if (r < n) dst[r] = (O)(add ? (float)dst[r] + v[r] : v[r]);
-  }
-}
 
 struct BlockOut {
   void* out;
@@ -231,17 +213,56 @@ __global__ __launch_bounds__(256 * WB, 3 - WB) void block_tile_kernel(BlockOps p
   const int nkb = (p.K + QB - 1) / QB;
   typename Main::Acc acc;
   Main::run(p, acc, n0, m0, g * per, min((g + 1) * per, nkb));
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  // A lane holds four neighbouring outputs of 8 NJ places; stored as they are,
+  // they would reach memory in 32- or 64-byte pieces (0.7 TB/s at 8,192 x
+  // 16,384 bf16).  Each wave turns its 16 NJ rows of 128 outputs round in LDS of
+  // its own instead, JG x 16 rows at a time, and stores whole rows: 16 bytes a
+  // lane, 128 sizeof(O) contiguous bytes a row.  The 16-byte chunks of a row are
+  // XOR-permuted by the row, so neither side meets a bank twice.
+  constexpr int NC = 8 * sizeof(O), E = OutPiece<O>::E;  // chunks of a row, outputs of a chunk
+  constexpr int JG = NJ * 16 * 128 * sizeof(O) > 16384 ? NJ / 2 : NJ;
+  constexpr int REGION = JG * 16 * 128 * sizeof(O);
+  constexpr int PER = Main::STAGE / REGION;              // waves' regions a stage holds
+  static_assert(2 * PER >= 4 * WB, "the stages hold every wave's region");
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  char* const lds = (w < PER ? Main::template stage<0>() : Main::template stage<1>()) + w % PER * REGION;
   O* const out = (O*)o.out + g * o.split;
+  const int col = lane & 15, quad = lane >> 4;
+  const int nw = n0 + (w >> 2) * 128, mw = m0 + (w & 3) * 16 * NJ;
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const int m = m0 + (w & 3) * 16 * NJ + j * 16 + (lane & 15);
-    if (m >= p.M) continue;
-    O* const row = out + (int64_t)m * o.ldo;
+  for (int jg = 0; jg < NJ; jg += JG) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int n = n0 + (w >> 2) * 128 + i * 16 + (lane >> 4) * 4;
-      store4(row + n, acc[i][j], p.N - n, o.add);
+    for (int j = 0; j < JG; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        struct __attribute__((aligned(4 * sizeof(O)))) Four {
+          O v[4];
+        } f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) f.v[r] = (O)acc[i][jg + j][r];
+        const int at = i * 16 + quad * 4;  // of the row
+        *(Four*)(lds + (j * 16 + col) * 128 * sizeof(O) + ((at / E) ^ col) * 16 + at % E * sizeof(O)) = f;
+      }
+    __builtin_amdgcn_s_waitcnt(WAIT_LGKM0);
+#pragma unroll
+    for (int x = 0; x < JG * 16 * NC / 64; ++x) {
+      const int row = x * (64 / NC) + lane / NC, ch = lane % NC;
+      const int m = mw + jg * 16 + row, n = nw + ch * E;
+      OutPiece<O> v = *(const OutPiece<O>*)__builtin_assume_aligned(
+          lds + row * 128 * sizeof(O) + (ch ^ (row & 15)) * 16, 16);
+      if (m >= p.M || n >= p.N) continue;
+      O* const dst = out + (int64_t)m * o.ldo + n;
+      if (n + E <= p.N) {
+        if (o.add) {
+          const OutPiece<O> old = *(const OutPiece<O>*)dst;
+#pragma unroll
+          for (int e = 0; e < E; ++e) v.v[e] = (O)((float)v.v[e] + (float)old.v[e]);
+        }
+        *(OutPiece<O>*)dst = v;
+      } else {
+        for (int e = 0; e < E; ++e)
+          if (n + e < p.N) dst[e] = (O)(o.add ? (float)dst[e] + (float)v.v[e] : (float)v.v[e]);
+      }
     }
   }
 }

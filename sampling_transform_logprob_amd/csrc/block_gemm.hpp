@@ -64,6 +64,9 @@ __device__ inline f32x4 block_mfma(const FragF16& a, const FragF16& b) {
   return p;
 }
 
+// s_waitcnt of the LDS counter alone (vmcnt at its largest)
+constexpr int WAIT_LGKM0 = 0xc07f;
+
 // Operands of the product.
 struct BlockOps {
   const uint8_t* a;
@@ -271,7 +274,9 @@ struct BlockMain {
     }
 #pragma unroll
     for (int idx = NM - LAG; idx < NM; ++idx) scale_in(idx, 1);
-    __builtin_amdgcn_s_waitcnt(WAIT_VM0_LGKM0);  // (no load may land after the workgroup has gone)
+    // the stages are free: no load of any wave is on its way, no read left
+    __builtin_amdgcn_s_waitcnt(WAIT_VM0_LGKM0);
+    __syncthreads();
   }
 };
 
