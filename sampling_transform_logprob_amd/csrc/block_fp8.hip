@@ -200,11 +200,12 @@ struct BlockOut {
   int add;
 };
 
-// 128 WB rows of b by 64 NJ rows of a per workgroup; segment g of the reduction
-// (blocks [g per, (g + 1) per)) goes to its own partial output.
-template <int NJ, bool ROWB, class F, int WB, class O>
-__global__ __launch_bounds__(256 * WB, 3 - WB) void block_tile_kernel(BlockOps p, BlockOut o, TileMap map, int per) {
-  using Main = BlockMain<NJ, ROWB, F, WB>;
+// One output tile per workgroup; segment g of the reduction (blocks [g per,
+// (g + 1) per)) goes to its own partial output.
+template <class Main, class O>
+__global__ __launch_bounds__(64 * Main::W, Main::W == 4 ? 2 : 1) void block_tile_kernel(BlockOps p, BlockOut o,
+                                                                                        TileMap map, int per) {
+  constexpr int NI = Main::NI, NJ = Main::NJ;
   const int tiles = map.tiles_m * map.tiles_n;
   const int g = blockIdx.x / tiles;
   int tn, tm;
@@ -213,35 +214,36 @@ __global__ __launch_bounds__(256 * WB, 3 - WB) void block_tile_kernel(BlockOps p
   const int nkb = (p.K + QB - 1) / QB;
   typename Main::Acc acc;
   Main::run(p, acc, n0, m0, g * per, min((g + 1) * per, nkb));
-  // A lane holds four neighbouring outputs of 8 NJ places; stored as they are,
+  // A lane holds four neighbouring outputs of NI NJ places; stored as they are,
   // they would reach memory in 32- or 64-byte pieces (0.7 TB/s at 8,192 x
-  // 16,384 bf16).  Each wave turns its 16 NJ rows of 128 outputs round in LDS of
-  // its own instead, JG x 16 rows at a time, and stores whole rows: 16 bytes a
-  // lane, 128 sizeof(O) contiguous bytes a row.  The 16-byte chunks of a row are
-  // XOR-permuted by the row, so neither side meets a bank twice.
-  constexpr int NC = 8 * sizeof(O), E = OutPiece<O>::E;  // chunks of a row, outputs of a chunk
-  constexpr int JG = NJ * 16 * 128 * sizeof(O) > 16384 ? NJ / 2 : NJ;
-  constexpr int REGION = JG * 16 * 128 * sizeof(O);
-  constexpr int PER = Main::STAGE / REGION;              // waves' regions a stage holds
-  static_assert(2 * PER >= 4 * WB, "the stages hold every wave's region");
+  // 16,384 bf16).  Each wave turns its 16 NJ rows of 16 NI outputs round in LDS
+  // of its own instead, 16 JG rows at a time, and stores whole rows, 16 bytes a
+  // lane.  The 16-byte chunks of a row are XOR-permuted by the row, so neither
+  // side meets a bank twice.
+  constexpr int ROW = 16 * NI * sizeof(O), NC = ROW / 16, E = OutPiece<O>::E;  // chunks of a row, outputs of a chunk
+  constexpr int MASK = NC < 16 ? NC - 1 : 15;
+  constexpr int JG = NJ * 16 * ROW > 16384 ? NJ / 2 : NJ;
+  constexpr int REGION = JG * 16 * ROW;
+  constexpr int PER = Main::STAGE / REGION;  // waves' regions a stage holds
+  static_assert(2 * PER >= Main::W, "the stages hold every wave's region");
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   char* const lds = (w < PER ? Main::template stage<0>() : Main::template stage<1>()) + w % PER * REGION;
   O* const out = (O*)o.out + g * o.split;
   const int col = lane & 15, quad = lane >> 4;
-  const int nw = n0 + (w >> 2) * 128, mw = m0 + (w & 3) * 16 * NJ;
+  const int nw = n0 + w / Main::WM * 16 * NI, mw = m0 + w % Main::WM * 16 * NJ;
 #pragma unroll
   for (int jg = 0; jg < NJ; jg += JG) {
 #pragma unroll
     for (int j = 0; j < JG; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < NI; ++i) {
         struct __attribute__((aligned(4 * sizeof(O)))) Four {
           O v[4];
         } f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) f.v[r] = (O)acc[i][jg + j][r];
         const int at = i * 16 + quad * 4;  // of the row
-        *(Four*)(lds + (j * 16 + col) * 128 * sizeof(O) + ((at / E) ^ col) * 16 + at % E * sizeof(O)) = f;
+        *(Four*)(lds + (j * 16 + col) * ROW + ((at / E) ^ (col & MASK)) * 16 + at % E * sizeof(O)) = f;
       }
     __builtin_amdgcn_s_waitcnt(WAIT_LGKM0);
 #pragma unroll
@@ -249,7 +251,7 @@ __global__ __launch_bounds__(256 * WB, 3 - WB) void block_tile_kernel(BlockOps p
       const int row = x * (64 / NC) + lane / NC, ch = lane % NC;
       const int m = mw + jg * 16 + row, n = nw + ch * E;
       OutPiece<O> v = *(const OutPiece<O>*)__builtin_assume_aligned(
-          lds + row * 128 * sizeof(O) + (ch ^ (row & 15)) * 16, 16);
+          lds + row * ROW + (ch ^ (row & MASK)) * 16, 16);
       if (m >= p.M || n >= p.N) continue;
       O* const dst = out + (int64_t)m * o.ldo + n;
       if (n + E <= p.N) {
@@ -286,15 +288,21 @@ __global__ __launch_bounds__(256) void block_zero_kernel(int64_t M, int64_t N, O
     out[e / N * ldo + e % N] = (O)0.0f;
 }
 
-// How a product is cut.  Large 16-bit outputs with tile scales take 256 x 256
-// tiles of eight waves (NJ = 4, the fewest operand bytes per product);
-// everything else four waves and 128 rows of b by 128 rows of a, or by 64 when
-// there are no more: two or three such workgroups share a compute unit and cover
-// each other's barriers.  Small M is bound by b's bytes, which those keep in
-// flight (5.8 TB/s of 151,936 x 5,120 codes for one row of a).  Segments of the
-// reduction fill the chip when there are few output tiles.
+// How a product is cut.
+//   M <= 64: 128 rows of b by 64 of a, four waves (128 x 16).  Bound by b's
+//     bytes, which three such workgroups a compute unit keep in flight (5.8 TB/s
+//     of 151,936 x 5,120 codes for one row of a).
+//   128 x 128, four waves: two workgroups share a compute unit and cover each
+//     other's barriers.  128 x 32 a wave on fp8 instructions; 64 x 64 on fp16
+//     ones, whose codes then are converted for twice the products.
+//   256 x 256, eight waves (128 x 64): 16-bit outputs with tile scales that make
+//     at least as good use of the compute units, in whole waves of tiles, as
+//     the 128 x 128 ones, which take 1.18 times as long for the same products
+//     (8,192 x 128,256 x 4,096: 3.90 against 4.61 ms; 2,048 x 4,096 x 4,096,
+//     an eighth of a wave: 57 against 39 us).
+// Segments of the reduction fill the chip when there are few output tiles.
 struct BlockPlan {
-  int nj;
+  int shape;  // 0: 128 x 64, 1: 128 x 128, 2: 256 x 256
   int64_t tiles_n, tiles_m;
   int S, per;  // segments, blocks per segment
 };
@@ -302,9 +310,13 @@ struct BlockPlan {
 BlockPlan plan_product(const stce_block_matmul& p) {
   BlockPlan b{};
   const int64_t nkb = ceil_div(p.K, QB);
-  b.nj = p.M <= 64 ? 1 : p.M > 128 && p.out_dtype != STCE_DT_F32 && p.b_rows == QB ? 4 : 2;
-  b.tiles_n = ceil_div(p.N, b.nj == 4 ? 256 : 128);
-  b.tiles_m = ceil_div(p.M, 64 * b.nj);
+  const int64_t small = ceil_div(p.N, 128) * ceil_div(p.M, 128), large = ceil_div(p.N, 256) * ceil_div(p.M, 256);
+  b.shape = p.M <= 64 ? 0 : 1;
+  if (p.M > 64 && p.out_dtype != STCE_DT_F32 && p.b_rows == QB &&
+      200 * ceil_div(large, 256) <= 118 * ceil_div(small, 512))
+    b.shape = 2;
+  b.tiles_n = ceil_div(p.N, b.shape == 2 ? 256 : 128);
+  b.tiles_m = ceil_div(p.M, 64 << b.shape);
   const int64_t wgs = b.tiles_n * b.tiles_m;
   int64_t S = 256 / wgs;  // (compute units; at least four blocks a segment)
   if (S > ceil_div(nkb, 4)) S = ceil_div(nkb, 4);
@@ -314,12 +326,11 @@ BlockPlan plan_product(const stce_block_matmul& p) {
   return b;
 }
 
-template <int NJ, bool ROWB, class F, class O>
+template <class Main, class O>
 void launch_tiles(const BlockPlan& b, const BlockOps& p, const BlockOut& o, hipStream_t s) {
-  constexpr int WB = NJ == 4 ? 2 : 1;
   const TileMap map{(int)b.tiles_n, (int)b.tiles_m, 4};
-  hipLaunchKernelGGL((block_tile_kernel<NJ, ROWB, F, WB, O>), dim3((unsigned)(b.tiles_n * b.tiles_m * b.S)),
-                     dim3(256 * WB), 0, s, p, o, map, b.per);
+  hipLaunchKernelGGL((block_tile_kernel<Main, O>), dim3((unsigned)(b.tiles_n * b.tiles_m * b.S)), dim3(64 * Main::W),
+                     0, s, p, o, map, b.per);
 }
 
 // A 16-bit output is rounded far above what the fp8 matrix instructions drop
@@ -329,12 +340,15 @@ void launch_tiles(const BlockPlan& b, const BlockOps& p, const BlockOut& o, hipS
 // products summed to 9e-9, at half the rate.
 template <bool ROWB, class O, class F>
 void launch_product(const BlockPlan& b, const BlockOps& p, const BlockOut& o, hipStream_t s) {
-  if constexpr (!ROWB && std::is_same<F, FragFp8>::value)
-    if (b.nj == 4) return launch_tiles<4, ROWB, F, O>(b, p, o, s);
-  if (b.nj == 1)
-    launch_tiles<1, ROWB, F, O>(b, p, o, s);
+  constexpr bool EXACT = std::is_same<F, FragF16>::value;
+  if constexpr (!ROWB && !EXACT)
+    if (b.shape == 2) return launch_tiles<BlockMain<8, 4, 2, 4, ROWB, F>, O>(b, p, o, s);
+  if (b.shape == 0)
+    launch_tiles<BlockMain<8, 1, 1, 4, ROWB, F>, O>(b, p, o, s);
+  else if constexpr (EXACT)
+    launch_tiles<BlockMain<4, 4, 2, 2, ROWB, F>, O>(b, p, o, s);
   else
-    launch_tiles<2, ROWB, F, O>(b, p, o, s);
+    launch_tiles<BlockMain<8, 2, 1, 4, ROWB, F>, O>(b, p, o, s);
 }
 
 unsigned sweep_blocks(int64_t n) { return (unsigned)(ceil_div(n, 256) < 8192 ? ceil_div(n, 256) : 8192); }

@@ -2,9 +2,9 @@
 // the reduction (gfx950): out[m, n] = sum_b sa[m, b] sb[n, b] P_b[m, n], P_b the
 // sum over the 128 k of block b.
 //
-// A workgroup of 4 WB waves forms 128 WB rows n of b by 64 NJ rows m of a; the
-// waves lie WB (n) x 4 (m), each 128 x 16 NJ outputs as 8 x NJ blocks of
-// 16 x 16, with b as the first matrix operand: a lane then holds one row m and
+// A workgroup's waves lie WN (n) x WM (m), each forming 16 NI rows n of b by
+// 16 NJ rows m of a as NI x NJ blocks of 16 x 16, with b as the first matrix
+// operand: a lane then holds one row m and
 // four consecutive n, so a per-tile scale of b is one value per wave, and an
 // output store four neighbours.  A k-tile is one scale block, 128 bytes of a
 // row; the loads, the LDS layout and its swizzle are those of the fp8 loop in
@@ -79,18 +79,21 @@ struct BlockOps {
   int M, N, K;
 };
 
-// NJ: 16-row blocks of a per wave.  ROWB: one scale per row of b (else per 128).
-// F: the fragment type, FragFp8 or FragF16.  WB: waves along n (4 WB in all).
-template <int NJ, bool ROWB, class F, int WB>
+// ROWB: one scale per row of b (else per 128).  F: the fragment type, FragFp8 or
+// FragF16.
+template <int NI_, int NJ_, int WN_, int WM_, bool ROWB_, class F_>
 struct BlockMain {
-  static constexpr int THREADS = 256 * WB;
-  static constexpr int TN = 128 * WB, TM = 64 * NJ;  // rows of b, of a per workgroup
-  static_assert(TM <= TN, "the scales of a take as many loads as those of b");
-  static constexpr int LB = 4, LA = 2 * NJ / WB;  // 1 KB loads per wave, operand and k-tile
+  static constexpr int NI = NI_, NJ = NJ_, WN = WN_, WM = WM_, W = WN * WM;
+  static constexpr bool ROWB = ROWB_;
+  typedef F_ F;
+  static constexpr int TN = 16 * NI * WN, TM = 16 * NJ * WM;  // rows of b, of a per workgroup
+  static_assert(TN <= 32 * W && TM <= 32 * W, "half the waves load an operand's scales, 64 rows each");
+  static_assert(NI % 4 == 0 && (ROWB || 128 % (16 * NI) == 0), "a wave's rows of b lie in one tile");
+  static constexpr int LB = TN / 8 / W, LA = TM / 8 / W;  // 1 KB loads per wave, operand and k-tile
   static constexpr int BYTES_B = TN * 128, BYTES_A = TM * 128;
   static constexpr int STAGE = BYTES_B + BYTES_A + 8 * TN;  // + TN scales each of b and of a
   static constexpr int OFF_A = BYTES_B, OFF_SB = BYTES_B + BYTES_A, OFF_SA = OFF_SB + 4 * TN;
-  typedef f32x4 Acc[8][NJ];
+  typedef f32x4 Acc[NI][NJ];
 
   // each stage an object of its own: the compiler then knows that the loads in
   // flight into one do not touch the others
@@ -104,7 +107,7 @@ struct BlockMain {
   __device__ static inline void run(const BlockOps& p, Acc& acc, int n0, int m0, int kt0, int kt1) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wb = w >> 2, wa = w & 3;
+    const int wb = w / WM, wa = w % WM;
     const int rowsB = min(p.N - n0, TN), rowsA = min(p.M - m0, TM);
     const int lda = (int)p.lda, ldb = (int)p.ldb;
     const __amdgpu_buffer_rsrc_t rb =
@@ -117,8 +120,8 @@ struct BlockMain {
     const int ce = lpc ^ lds_swz(lrow), co = lpc ^ lds_swz(lrow + 8);
     const int rB = (w * LB * 8 + lrow) * ldb, rA = (w * LA * 8 + lrow) * lda;
     // scales: the first half of the waves loads 64 rows each of b's, the others of a's
-    const bool isb = w < 2 * WB;
-    const int sw0 = (w & (2 * WB - 1)) * 64, srow = sw0 + lane;
+    const bool isb = w < W / 2;
+    const int sw0 = w % (W / 2) * 64, srow = sw0 + lane;
     const int nbase = ROWB ? n0 : n0 >> 7;
     const int soff = isb ? ((ROWB ? min(n0 + srow, p.N - 1) : min(n0 + srow, p.N - 1) >> 7) - nbase) * p.sb_row * 4
                          : min(srow, rowsA - 1) * p.sa_row * 4;
@@ -154,25 +157,23 @@ struct BlockMain {
       for (int x = 0; x < LOADS; ++x) issue(sg_c, kt, x);
     };
     const int frow = lane & 15, fq = lane >> 4, sw = lds_swz(frow);
-    const int offB = (wb * 128 + frow) * 128, offA = OFF_A + (wa * 16 * NJ + frow) * 128;
+    const int offB = (wb * 16 * NI + frow) * 128, offA = OFF_A + (wa * 16 * NJ + frow) * 128;
     const int c0 = ((2 * fq) ^ sw) * 16, c1 = ((2 * fq + 1) ^ sw) * 16;
     auto frag = [&](const char* base) __attribute__((always_inline)) {
       return raw_frag(*(const u32x4*)(base + c0), *(const u32x4*)(base + c1));
     };
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{};
     // Fragments: a's NJ of a tile, reloaded for the next one behind their last
-    // use; b's eight through a ring of four, read AHEAD blocks ahead (with, for
+    // use; b's NI through a ring of four, read AHEAD blocks ahead (with, for
     // row scales, the lane's four scales of b).  The results of the matrix
     // instructions wait in a ring too and are scaled in LAG instructions later,
     // across the tile's end, with that tile's scales (s by stage).
-    constexpr int LAG = 3, NM = 8 * NJ, AHEAD = NJ == 4 ? 2 : 3;
-    // of one 16 x 16 x 128 step: matrix instructions, ordinary ones
-    constexpr int MPB = std::is_same<F, FragFp8>::value ? 1 : 4, VPB = ROWB ? 8 : 4;
+    constexpr int LAG = 3, NM = NI * NJ, AHEAD = NJ == 4 ? 2 : 3;
     Raw fa[NJ], fb[4];
-    f32x4 sbv[8];  // (used LAG instructions later: no ring)
+    f32x4 sbv[NI];  // (used LAG instructions later: no ring)
     f32x4 part[4];
     float s[2][NJ];
 #pragma unroll
@@ -180,7 +181,7 @@ struct BlockMain {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) s[0][j] = s[1][j] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sbv[i] = f32x4{};
+    for (int i = 0; i < NI; ++i) sbv[i] = f32x4{};
     auto scale_in = [&](int idx, int sg) __attribute__((always_inline)) {  // idx: instruction of the tile of stage sg
       const int i = idx / NJ, j = idx % NJ;
 #pragma unroll
@@ -195,7 +196,7 @@ struct BlockMain {
     auto read_b = [&](const char* st, int i, bool live) __attribute__((always_inline)) {
       fb[i & 3] = frag(st + offB + i * 16 * 128);
       if constexpr (ROWB) {
-        sbv[i] = *(const f32x4*)(st + OFF_SB + (wb * 128 + i * 16 + fq * 4) * 4);
+        sbv[i] = *(const f32x4*)(st + OFF_SB + (wb * 16 * NI + i * 16 + fq * 4) * 4);
 #pragma unroll
         for (int r = 0; r < 4; ++r) sbv[i][r] = live ? sbv[i][r] : 0.0f;
       }
@@ -206,7 +207,7 @@ struct BlockMain {
       const float* sa = (const float*)(st + OFF_SA) + wa * 16 * NJ + frow;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) rsa[j] = sa[j * 16];
-      if constexpr (!ROWB) rsb = *((const float*)(st + OFF_SB) + wb * 128);
+      if constexpr (!ROWB) rsb = *((const float*)(st + OFF_SB) + wb * 16 * NI);
     };
     auto set_scales = [&](int sg, bool live) __attribute__((always_inline)) {
 #pragma unroll
@@ -224,17 +225,17 @@ struct BlockMain {
       for (int idx = 0; idx < NM; ++idx) {
         const int i = idx / NJ, j = idx % NJ;
         if (j == 0) {
-          if (i == 8 - AHEAD) {
+          if (i == NI - AHEAD) {
             // every wave has read all of this stage, and the next tile has landed
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_waitcnt(WAIT_VM0_LGKM0);
             __syncthreads();
             __builtin_amdgcn_sched_barrier(0);
           }
-          if (i + AHEAD < 8)
+          if (i + AHEAD < NI)
             read_b(st, i + AHEAD, kt < kt1);
           else
-            read_b(nx, i + AHEAD - 8, kt + 1 < kt1);
+            read_b(nx, i + AHEAD - NI, kt + 1 < kt1);
           cb = F(fb[i & 3]);
         }
         // (of the tile before: its instruction NM + idx - LAG)
@@ -244,12 +245,12 @@ struct BlockMain {
         if (idx == 0) set_scales(sg, kt < kt1);
         // behind the barrier: the loads of the tile after the next one into the
         // stage just freed, a few behind every matrix instruction
-        constexpr int FIRST = (8 - AHEAD) * NJ, PER = (LOADS + NM - FIRST - 1) / (NM - FIRST);
+        constexpr int FIRST = (NI - AHEAD) * NJ, PER = (LOADS + NM - FIRST - 1) / (NM - FIRST);
 #pragma unroll
         for (int x = 0; x < PER; ++x)
           if (idx >= FIRST && (idx - FIRST) * PER + x < LOADS) issue(sg_c, kt + 2, (idx - FIRST) * PER + x);
         if (idx == FIRST) read_scales(nx);
-        if (i == 7) fa[j] = frag(nx + offA + j * 16 * 128);
+        if (i == NI - 1) fa[j] = frag(nx + offA + j * 16 * 128);
         __builtin_amdgcn_sched_barrier(0);
       }
       __builtin_amdgcn_sched_barrier(0);
