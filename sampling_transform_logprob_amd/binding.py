@@ -9,6 +9,7 @@ entry point raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -654,11 +655,13 @@ def _rows(name, x, dtypes):
         raise ValueError(f"{name} must be a 2-d tensor")
     if x.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {tuple(str(d) for d in dtypes)}, got {x.dtype}")
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError(f"{name} must be on a GPU, got {x.device}")
     R, C = x.shape
+    if x.is_contiguous():
+        return x, C
     if (C > 1 and x.stride(1) != 1) or (R > 1 and x.stride(0) < C):
-        x = x.contiguous()
+        return x.contiguous(), C
     return x, (x.stride(0) if R > 1 and C else C)
 
 
@@ -680,12 +683,21 @@ def _token_problem(logits, tokens, temperature, top_n, ignore_index):
     T, V = z.shape
     dev = z.device
     tok, K = _tokens(tokens, T, dev)
-    temp = _meta("temperature", temperature, T, torch.float32, dev)
+    temp = None if temperature is None else _meta("temperature", temperature, T, torch.float32, dev)
     prob = TokenProblem(T, V, VALUE_DTYPES[z.dtype], 0 if ignore_index is None else PROBLEM_IGNORE_INDEX,
-                        z.data_ptr(), max(ld, V), None if temp is None else temp.data_ptr(),
+                        z.data_ptr(), ld if ld > V else V, None if temp is None else temp.data_ptr(),
                         None if tok is None else tok.data_ptr(), K, top_n,
                         0 if ignore_index is None else int(ignore_index))
     return prob, (z, tok, temp)
+
+
+@functools.lru_cache(maxsize=1024)
+def _token_workspace(T, V, dtype, top_n):
+    """Workspace bytes of ``stce_token_logprobs`` for these sizes."""
+    nb = ctypes.c_size_t()
+    prob = TokenProblem(T, V, dtype, 0, None, V, None, None, 0, top_n, 0)
+    _check(load().stce_token_workspace_bytes(ctypes.byref(prob), ctypes.byref(nb)))
+    return nb.value
 
 
 def token_logprobs(logits, tokens=None, temperature=None, *, top_n: int = 0, ignore_index: Optional[int] = None,
@@ -706,10 +718,10 @@ def token_logprobs(logits, tokens=None, temperature=None, *, top_n: int = 0, ign
     T, K = prob.T, prob.K
     dev = logits.device
     L = load()
-    nb = ctypes.c_size_t()
-    _check(L.stce_token_workspace_bytes(ctypes.byref(prob), ctypes.byref(nb)))
-    if workspace is None and nb.value:
-        workspace = torch.empty(nb.value, dtype=torch.uint8, device=dev)
+    if workspace is None:
+        nb = _token_workspace(T, prob.V, prob.dtype, top_n)
+        if nb:
+            workspace = torch.empty(nb, dtype=torch.uint8, device=dev)
     # one allocation for the fp32 outputs: a row costs little more than its calls
     buf = torch.empty(T * (6 + K + top_n), dtype=torch.float32, device=dev)
     out = dict(stats=buf.as_strided((T, 4), (4, 1), 0), lse=buf.as_strided((T,), (1,), 4 * T),
@@ -808,12 +820,12 @@ def fp8_quantize_blocks(x: torch.Tensor, *, block: str = "row", transpose: bool 
     dev = x.device
     kp = -(-n // 16) * 16
     codes = torch.empty(Q, kp, dtype=torch.float8_e4m3fn, device=dev)
-    scales = torch.empty(-(-n // FP8_BLOCK), Q if block == "row" else -(-Q // FP8_BLOCK), dtype=torch.float32,
-                         device=dev)
+    sr = Q if block == "row" else -(-Q // FP8_BLOCK)
+    scales = torch.empty_strided((sr, -(-n // FP8_BLOCK)), (1, sr), dtype=torch.float32, device=dev)
     flags = (QUANT_TILE if block == "tile" else 0) | (QUANT_TRANSPOSE if transpose else 0)
     _call(load().stce_fp8_quantize_blocks, dev, _ptr(x), VALUE_DTYPES[x.dtype], R, C, max(ld, C), flags, _ptr(codes),
           kp, _ptr(scales))
-    return codes, scales.t()
+    return codes, scales
 
 
 def _fp8_operand(name, q, scale, tile_ok):
