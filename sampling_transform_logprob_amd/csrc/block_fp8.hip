@@ -289,12 +289,13 @@ __global__ __launch_bounds__(256) void block_zero_kernel(int64_t M, int64_t N, O
 }
 
 // How a product is cut.
-//   M <= 64: 128 rows of b by 64 of a, four waves (128 x 16).  Bound by b's
+//   M <= 64: 128 rows of b by 64 of a, four waves (64 x 32).  Bound by b's
 //     bytes, which three such workgroups a compute unit keep in flight (5.8 TB/s
 //     of 151,936 x 5,120 codes for one row of a).
-//   128 x 128, four waves: two workgroups share a compute unit and cover each
-//     other's barriers.  128 x 32 a wave on fp8 instructions; 64 x 64 on fp16
-//     ones, whose codes then are converted for twice the products.
+//   128 x 128, four waves (64 x 64): two workgroups share a compute unit and
+//     cover each other's barriers.  (Waves of 128 x 32 read and convert more
+//     fragments a product: 588 against 538 us for 32,000 x 2,048 x 4,096 to
+//     fp32 with row scales.)
 //   256 x 256, eight waves (128 x 64): 16-bit outputs with tile scales that make
 //     at least as good use of the compute units, in whole waves of tiles, as
 //     the 128 x 128 ones, which take 1.18 times as long for the same products
@@ -344,11 +345,9 @@ void launch_product(const BlockPlan& b, const BlockOps& p, const BlockOut& o, hi
   if constexpr (!ROWB && !EXACT)
     if (b.shape == 2) return launch_tiles<BlockMain<8, 4, 2, 4, ROWB, F>, O>(b, p, o, s);
   if (b.shape == 0)
-    launch_tiles<BlockMain<8, 1, 1, 4, ROWB, F>, O>(b, p, o, s);
-  else if constexpr (EXACT)
-    launch_tiles<BlockMain<4, 4, 2, 2, ROWB, F>, O>(b, p, o, s);
+    launch_tiles<BlockMain<4, 2, 2, 2, ROWB, F>, O>(b, p, o, s);
   else
-    launch_tiles<BlockMain<8, 2, 1, 4, ROWB, F>, O>(b, p, o, s);
+    launch_tiles<BlockMain<4, 4, 2, 2, ROWB, F>, O>(b, p, o, s);
 }
 
 unsigned sweep_blocks(int64_t n) { return (unsigned)(ceil_div(n, 256) < 8192 ? ceil_div(n, 256) : 8192); }

@@ -87,7 +87,7 @@ struct BlockMain {
   static constexpr bool ROWB = ROWB_;
   typedef F_ F;
   static constexpr int TN = 16 * NI * WN, TM = 16 * NJ * WM;  // rows of b, of a per workgroup
-  static_assert(TN <= 32 * W && TM <= 32 * W, "half the waves load an operand's scales, 64 rows each");
+  static_assert(TN == 32 * W && TM <= TN, "half the waves load the scales of TN rows of an operand, 64 each");
   static_assert(NI % 4 == 0 && (ROWB || 128 % (16 * NI) == 0), "a wave's rows of b lie in one tile");
   static constexpr int LB = TN / 8 / W, LA = TM / 8 / W;  // 1 KB loads per wave, operand and k-tile
   static constexpr int BYTES_B = TN * 128, BYTES_A = TM * 128;
@@ -173,7 +173,12 @@ struct BlockMain {
     // across the tile's end, with that tile's scales (s by stage).
     constexpr int LAG = 3, NM = NI * NJ, AHEAD = NJ == 4 ? 2 : 3;
     Raw fa[NJ], fb[4];
-    f32x4 sbv[NI];  // (used LAG instructions later: no ring)
+    // Row scales of b wait as long as the results they scale: block i's may be
+    // read anew (AHEAD blocks ahead) only when the last result of its previous
+    // tile is in, LAG instructions after that; where it comes too early, the two
+    // tiles' scales take slots by parity.
+    constexpr int SLOTS = (NI - AHEAD) * NJ >= NJ + LAG ? NI : 2 * NI;
+    f32x4 sbv[SLOTS];
     f32x4 part[4];
     float s[2][NJ];
 #pragma unroll
@@ -181,24 +186,25 @@ struct BlockMain {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) s[0][j] = s[1][j] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) sbv[i] = f32x4{};
+    for (int i = 0; i < SLOTS; ++i) sbv[i] = f32x4{};
     auto scale_in = [&](int idx, int sg) __attribute__((always_inline)) {  // idx: instruction of the tile of stage sg
       const int i = idx / NJ, j = idx % NJ;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float v = ROWB ? part[idx & 3][r] * sbv[i][r] : part[idx & 3][r];
+        const float v = ROWB ? part[idx & 3][r] * sbv[(SLOTS > NI ? sg * NI : 0) + i][r] : part[idx & 3][r];
         acc[i][j][r] = __builtin_fmaf(v, s[sg][j], acc[i][j][r]);
       }
       // holds the sums here: left free, the compiler collects all of a tile's
       // products before it adds them, and runs out of registers
       asm volatile("" : "+v"(acc[i][j]));
     };
-    auto read_b = [&](const char* st, int i, bool live) __attribute__((always_inline)) {
+    auto read_b = [&](const char* st, int sg, int i, bool live) __attribute__((always_inline)) {
       fb[i & 3] = frag(st + offB + i * 16 * 128);
       if constexpr (ROWB) {
-        sbv[i] = *(const f32x4*)(st + OFF_SB + (wb * 16 * NI + i * 16 + fq * 4) * 4);
+        f32x4 v = *(const f32x4*)(st + OFF_SB + (wb * 16 * NI + i * 16 + fq * 4) * 4);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sbv[i][r] = live ? sbv[i][r] : 0.0f;
+        for (int r = 0; r < 4; ++r) v[r] = live ? v[r] : 0.0f;
+        sbv[(SLOTS > NI ? sg * NI : 0) + i] = v;
       }
     };
     // scales of a tile: read as they lie once it has landed, multiplied when it starts
@@ -233,9 +239,9 @@ struct BlockMain {
             __builtin_amdgcn_sched_barrier(0);
           }
           if (i + AHEAD < NI)
-            read_b(st, i + AHEAD, kt < kt1);
+            read_b(st, sg, i + AHEAD, kt < kt1);
           else
-            read_b(nx, i + AHEAD - NI, kt + 1 < kt1);
+            read_b(nx, 1 - sg, i + AHEAD - NI, kt + 1 < kt1);
           cb = F(fb[i & 3]);
         }
         // (of the tile before: its instruction NM + idx - LAG)
@@ -266,7 +272,7 @@ struct BlockMain {
     __syncthreads();
     read_scales(stage<0>());
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) read_b(stage<0>(), i, true);
+    for (int i = 0; i < AHEAD; ++i) read_b(stage<0>(), 0, i, true);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) fa[j] = frag(stage<0>() + offA + j * 16 * 128);
     for (int kt = kt0; kt < kt1; kt += 2) {
