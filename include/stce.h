@@ -606,7 +606,7 @@ stce_status stce_token_logprobs_backward(const stce_token_problem *prob, const f
  * With Y of Q rows and L columns:
  *   blocks:  128 consecutive columns of one row, or, with STCE_QUANT_TILE,
  *            tiles of 128 rows x 128 columns (the last ones shorter);
- *   scale  = fl32(largest |y| of the block / 448), 1 where that is 0;
+ *   scale  = fl32(largest |y| of the block * fl32(1 / 448)), 1 where that is 0;
  *   code   = e4m3(clamp(fl32(y / scale), -448, 448)), nearest, ties to even.
  * A block that holds a NaN or an infinity gets scale NaN and codes 0, so every
  * product with it is NaN.  Writes codes [Q, round_up(L, 16)] (columns past L

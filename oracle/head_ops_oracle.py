@@ -115,7 +115,7 @@ def quantize_blocks(x, block="row", transpose=False):
             if not np.isfinite(v).all():
                 scales[i, j] = np.nan
                 continue
-            a = np.float32(np.abs(v).max() / np.float32(E4M3_MAX))
+            a = np.float32(np.abs(v).max() * np.float32(1 / E4M3_MAX))
             scales[i, j] = a if a > 0 else np.float32(1)
             q = np.clip((v / scales[i, j]).astype(np.float32), -E4M3_MAX, E4M3_MAX)
             codes[i * rows:i * rows + v.shape[0], j * BLOCK:j * BLOCK + v.shape[1]] = e4m3_nearest(q)

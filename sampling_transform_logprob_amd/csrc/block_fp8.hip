@@ -11,7 +11,7 @@ constexpr int QB = 128;  // values per scale along the reduction
 
 // A block's scale a, and what its codes are formed with.  The codes need
 // fl32(v / a) exactly only where |v / a| >= 2^-11 (below, every code is a zero),
-// and |v| <= 448 a (1 + 2^-24): there the correction step of quot_fast (see
+// and |v| <= 448 a (1 + 2^-22): there the correction step of quot_fast (see
 // there) gives the correctly rounded quotient as long as ulp(v / a) ulp(a) and
 // the reciprocal stay in range, for a in [2^-92, 2^125]; a smaller a and its
 // values are first multiplied by f = 2^100, which is exact.  The largest a is
@@ -25,7 +25,7 @@ struct BlockScale {
 __device__ inline BlockScale block_scale(float mx) {
   BlockScale b;
   b.finite = mx < __builtin_huge_valf();
-  const float q = mx / E4M3_MAX;
+  const float q = mx * (1.0f / E4M3_MAX);
   b.a = !b.finite ? __builtin_nanf("") : q == 0.0f ? 1.0f : q;
   b.f = b.a < 0x1p-92f ? 0x1p100f : 1.0f;
   b.af = b.a * b.f;
