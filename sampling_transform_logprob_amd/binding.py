@@ -637,6 +637,38 @@ class ScoreFunction(torch.autograd.Function):
 # quantization and product.  Their arrays may lie on any GPU: the call is made
 # on the arrays' device, on its current stream.
 # ---------------------------------------------------------------------------
+_fast = None
+
+
+def _load_fast():
+    """The marshalling module (see csrc/marshal.cpp) with the library's
+    functions bound, or False where it is not built.  It makes the calls below
+    with less host time for operands it takes as they stand; everything else,
+    and every error, goes through the ctypes calls."""
+    global _fast
+    L = load()
+    try:
+        from . import _marshal as m
+    except ImportError:
+        _fast = False
+    else:
+        m.bind({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in SYMBOLS[-6:]})
+        _fast = m
+    return _fast
+
+
+def _here(x):
+    """(module, device index) of the marshalling module where it can take a call
+    on x's device: the current one."""
+    m = _fast
+    if m is None:
+        m = _load_fast()
+    if m is False or not isinstance(x, torch.Tensor) or not x.is_cuda:
+        return None, 0
+    i = x.get_device()
+    return (m, i) if i == torch._C._cuda_getDevice() else (None, 0)
+
+
 def _call(fn, dev, *args):
     """fn(*args, stream) on the arrays' device, on its current stream."""
     # (the raw queries: a torch.cuda.Stream object costs as much as a launch)
@@ -714,6 +746,16 @@ def token_logprobs(logits, tokens=None, temperature=None, *, top_n: int = 0, ign
     last token with a logit above -inf).  Masked tokens (-inf) score -inf;
     ``ignore_index`` scores 0.  ``check=False`` skips the report of invalid
     tokens and temperatures, which reads one number back from the GPU."""
+    if workspace is None:
+        m, i = _here(logits)
+        r = m and m.token_logprobs(logits, tokens, temperature, top_n, ignore_index, check, i,
+                                   torch._C._cuda_getCurrentRawStream(i))
+        if r is not None:
+            if r[0]:
+                _check(r[0])
+            if check:
+                _raise_rows(r[2], "stce_token_logprobs", dict(temperature=temperature, target=tokens))
+            return r[1]
     prob, keep = _token_problem(logits, tokens, temperature, top_n, ignore_index)
     T, K = prob.T, prob.K
     dev = logits.device
@@ -751,8 +793,16 @@ def token_logprobs_backward(logits, tokens, stats, grad_logprob=None, grad_entro
     + sum(grad_lse * lse)`` with respect to the logits, in their dtype; ``stats``
     is the forward's.  ``grad_logits`` gives the result's place (strided rows
     allowed; not overlapping the logits)."""
+    if grad_logits is None:
+        m, i = _here(logits)
+        r = m and m.token_grad(logits, tokens, stats, grad_logprob, grad_entropy, grad_lse, temperature, ignore_index,
+                               i, torch._C._cuda_getCurrentRawStream(i))
+        if r is not None:
+            if r[0]:
+                _check(r[0])
+            return r[1]
     prob, keep = _token_problem(logits, tokens, temperature, 0, ignore_index)
-    T, V, K = prob.T, prob.V, prob.K
+    T, V = prob.T, prob.V
     dev = logits.device
     if stats.shape != (T, 4) or stats.dtype != torch.float32 or stats.device != dev or not stats.is_contiguous():
         raise ValueError("stats must be the contiguous fp32 [T, 4] tensor of the forward")
@@ -814,6 +864,12 @@ def fp8_quantize_blocks(x: torch.Tensor, *, block: str = "row", transpose: bool 
     index slowest in memory.)"""
     if block not in ("row", "tile"):
         raise ValueError("block must be 'row' or 'tile'")
+    m, i = _here(x)
+    r = m and m.quantize(x, block == "tile", transpose, i, torch._C._cuda_getCurrentRawStream(i))
+    if r is not None:
+        if r[0]:
+            _check(r[0])
+        return r[1], r[2]
     x, ld = _rows("x", x, VALUE_DTYPES)
     R, C = x.shape
     Q, n = (C, R) if transpose else (R, C)
@@ -856,6 +912,13 @@ def fp8_block_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, *, out: O
     [ceil(N / 128), ceil(K / 128)], fp32, any strides.  Returns ``out`` [M, N] in
     ``out_dtype`` (bf16, fp16, fp32), rounded once from fp32 sums; with
     ``accumulate`` the product is added to ``out`` (fp32)."""
+    if out is None and not accumulate and workspace is None:
+        m, i = _here(a)
+        r = m and m.matmul(a, a_scale, b, b_scale, out_dtype, i, torch._C._cuda_getCurrentRawStream(i))
+        if r is not None:
+            if r[0]:
+                _check(r[0])
+            return r[1]
     a, lda, _ = _fp8_operand("a", a, a_scale, False)
     b, ldb, b_rows = _fp8_operand("b", b, b_scale, True)
     M, K = a.shape

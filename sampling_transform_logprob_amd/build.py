@@ -1,4 +1,5 @@
-"""Build ``libstce.so`` (HIP, gfx950) in-tree with hipcc."""
+"""Build ``libstce.so`` (HIP, gfx950) in-tree with hipcc, and the host-only
+argument marshalling module ``_marshal.so`` with the C++ compiler."""
 from __future__ import annotations
 
 import os
@@ -8,6 +9,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libstce.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 SOURCES = ["kernels.hip", "select.hip", "sparse.hip", "api.hip", "token_logprob.hip", "block_fp8.hip",
            "ops_api.hip"]
 
@@ -52,7 +54,31 @@ def build(verbose: bool = False) -> str:
         os.remove(LIB + ".tmp")
         raise RuntimeError("kernels with private scratch memory: " + ", ".join(f"{n} ({b} B/lane)" for n, b in bad))
     os.replace(LIB + ".tmp", LIB)
+    build_marshal(verbose)
     return LIB
+
+
+def build_marshal(verbose: bool = False) -> str:
+    """The host-only Python module of csrc/marshal.cpp (argument marshalling;
+    torch's headers, no GPU code)."""
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-I{inc}", f"-I{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}",
+           f"-I{sysconfig.get_paths()['include']}", os.path.join(CSRC, "marshal.cpp"), "-o", MARSHAL + ".tmp",
+           f"-L{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError("g++ failed building _marshal.so")
+    os.replace(MARSHAL + ".tmp", MARSHAL)
+    return MARSHAL
 
 
 if __name__ == "__main__":

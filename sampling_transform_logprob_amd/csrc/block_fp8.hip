@@ -329,7 +329,7 @@ BlockPlan plan_product(const stce_block_matmul& p) {
 
 template <class Main, class O>
 void launch_tiles(const BlockPlan& b, const BlockOps& p, const BlockOut& o, hipStream_t s) {
-  const TileMap map{(int)b.tiles_n, (int)b.tiles_m, 4};
+  const TileMap map{(int)b.tiles_n, (int)b.tiles_m, 8};
   hipLaunchKernelGGL((block_tile_kernel<Main, O>), dim3((unsigned)(b.tiles_n * b.tiles_m * b.S)), dim3(64 * Main::W),
                      0, s, p, o, map, b.per);
 }

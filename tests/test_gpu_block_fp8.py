@@ -279,3 +279,36 @@ def test_refusals(rng):
         mm(a, sa, b, sb, out=torch.empty(4, 300, dtype=torch.bfloat16, device=dev()), accumulate=True)
     with pytest.raises(ValueError, match="out must be"):
         mm(a, sa, b, sb, out=torch.empty(4, 301, device=dev()))
+
+
+def test_both_marshalling_paths_agree(rng, monkeypatch):
+    """The marshalling module and the ctypes calls make the same call."""
+    def run_all():
+        x = torch.from_numpy(rng.standard_normal((70, 200)).astype(np.float32)).to(dev())
+        out = list(binding.fp8_quantize_blocks(x)) + list(binding.fp8_quantize_blocks(x, block="tile", transpose=True))
+        q, s = binding.fp8_quantize_blocks(x[:, ::2])                   # a copy is needed
+        w, ws = binding.fp8_quantize_blocks(torch.from_numpy(rng.standard_normal((300, 100)).astype(np.float32)).to(dev()),
+                                            block="tile")
+        out += [q, s, w, ws] + [binding.fp8_block_matmul(q, s, w, ws, d) for d in DT.values()]
+        z = torch.from_numpy(rng.standard_normal((9, 300)).astype(np.float32)).to(dev())
+        tok = torch.from_numpy(rng.integers(0, 300, (9, 3))).to(dev())
+        temp = torch.full((9,), 0.7, device=dev())
+        for zz, tt in ((z, tok), (z[:, 3:290], tok.clamp(max=200)[:, 0])):
+            for n in (0, 4):
+                o = binding.token_logprobs(zz, tt, temp, top_n=n, ignore_index=-100)
+                out += [o[k] for k in sorted(o)]
+            out.append(binding.token_logprobs_backward(zz, tt, o["stats"], torch.ones(tt.shape, device=dev()), temp, None,
+                                                       temperature=temp, ignore_index=-100))
+        out.append(binding.token_logprobs(z)["lse"])
+        return out
+    assert binding._load_fast() is not False, "the marshalling module is not built"
+    state = rng.bit_generator.state
+    a = run_all()
+    monkeypatch.setattr(binding, "_fast", False)
+    rng.bit_generator.state = state
+    b = run_all()
+    assert len(a) == len(b)
+    for x, y in zip(a, b):
+        assert x.shape == y.shape and x.dtype == y.dtype and x.stride() == y.stride()
+        xb, yb = (t.contiguous().reshape(-1).view(torch.uint8) for t in (x, y))
+        assert torch.equal(xb, yb)
