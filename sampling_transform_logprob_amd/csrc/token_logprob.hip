@@ -50,7 +50,13 @@ __device__ inline void rank_list(TopScratch& s, int n) {
   for (int i = threadIdx.x; i < cnt; i += TW) {
     const uint64_t mine = s.list[i];
     int rank = 0;
-    for (int j = 0; j < cnt; ++j) rank += s.list[j] > mine ? 1 : 0;
+    for (int j = 0; j < cnt; j += 8) {  // (eight reads in flight; what lies past cnt does not count)
+      uint64_t o[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) o[q] = s.list[j + q];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) rank += (j + q < cnt) & (o[q] > mine);
+    }
     if (rank < n) s.sorted[rank] = mine;
   }
   __syncthreads();
@@ -88,6 +94,24 @@ __device__ void scan_top(const Z* z, int64_t j0, int64_t j1, int n, TopScratch& 
   rank_list(s, n);
 }
 
+// Appends a thread's elements that reach `bar` (finite) to the list, as far as it
+// goes: one counter access for all of them.
+template <int N, class Id>
+__device__ inline void push_hits(TopScratch& s, float bar, const float* x, Id id) {
+  int hits = 0;
+#pragma unroll
+  for (int e = 0; e < N; ++e) hits += x[e] >= bar;
+  if (!hits) return;
+  int at = atomicAdd(&s.count, hits);
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    if (x[e] >= bar) {
+      if (at < LIST_CAP) s.list[at] = composite(order_key(x[e]), id(e));
+      ++at;
+    }
+  }
+}
+
 // Sum (or maximum) over the workgroup in a fixed order; every thread gets it.
 template <bool MAX>
 __device__ inline float block_reduce(float v, float* red) {
@@ -114,9 +138,25 @@ struct RowOut {
   int64_t* status;
 };
 
+// A thread's first given token and its logit, loaded while the row is: at the end
+// the two dependent loads would be waited for.
+struct Given {
+  int64_t y;
+  float z;
+};
+template <class Z>
+__device__ inline Given load_given(const RowOut& r, const Z* z, int64_t t, int i) {
+  Given g{-1, 0.0f};
+  if (i < r.K) {
+    g.y = r.tokens[t * r.K + i];
+    if (g.y >= 0 && g.y < r.V) g.z = to_f32(z[g.y]);
+  }
+  return g;
+}
+
 template <class Z>
 __device__ inline void write_row(const RowOut& r, const Z* z, int64_t t, float temp, float m, float S, float E,
-                                 const uint64_t* sorted, int tid, int nthreads) {
+                                 const uint64_t* sorted, Given given, int tid, int nthreads) {
   const float nan = __builtin_nanf("");
   const bool bad_t = bad_temperature(temp);
   const bool bad = bad_t || S != S || m == __builtin_huge_valf();
@@ -135,7 +175,8 @@ __device__ inline void write_row(const RowOut& r, const Z* z, int64_t t, float t
     }
   }
   for (int i = tid; i < r.K; i += nthreads) {
-    const int64_t y = r.tokens[t * r.K + i];
+    if (i != tid) given = load_given(r, z, t, i);
+    const int64_t y = given.y;
     float lp;
     if (r.ignore && y == r.ignore_index) {
       lp = 0.0f;
@@ -145,7 +186,7 @@ __device__ inline void write_row(const RowOut& r, const Z* z, int64_t t, float t
     } else if (bad || empty) {
       lp = bad ? nan : NEG_INF;
     } else {
-      lp = fminf((to_f32(z[y]) - m) / temp - LN2 * l2, 0.0f);
+      lp = fminf((given.z - m) / temp - LN2 * l2, 0.0f);
     }
     if (r.o.logprob) r.o.logprob[t * r.K + i] = lp;
   }
@@ -216,6 +257,25 @@ __device__ inline uint32_t nth_key(const uint32_t (&key)[NK], int n) {
   return k;
 }
 
+// A lower bound of the n-th largest of at least n values (n <= 256), given as 256
+// values or maxima of disjoint groups of them, v[q] of lane l the (64 q + l)-th:
+// the n-th largest, or, for few n, the n-th largest of the 64 lanes' maxima (a
+// quarter of the counting, which costs about ten cycles an instruction; it lets a
+// fifth more values through at n = 20).  Never -inf: what reaches the bound is
+// above it.
+template <int SHIFT>
+__device__ inline float nth_bound(const float (&v)[4], int n) {
+  uint32_t k;
+  if (n <= 48) {
+    const uint32_t key[1] = {order_key(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])))};
+    k = nth_key<SHIFT>(key, n);
+  } else {
+    const uint32_t key[4] = {order_key(v[0]), order_key(v[1]), order_key(v[2]), order_key(v[3])};
+    k = nth_key<SHIFT>(key, n);
+  }
+  return key_value(k < KEY_LOWEST ? KEY_LOWEST : k);
+}
+
 // Maximum and sums of a part of a row relative to that maximum.
 struct Partial {
   float m, S, E, pad;
@@ -253,8 +313,8 @@ constexpr int CELL_CAP = 512;  // cells that may hold alternatives
 // elements of tpc consecutive tiles: its maximum.  The n-th largest of the 256
 // threads' maxima is a lower bound of the n-th largest element, and little more
 // than n elements reach it (20.8 expected of 8,192 random ones for n = 20), so
-// after the loop only the cells that reach the bound are read again and their
-// elements above it ranked.  Rows whose ties overflow the lists take scan_top.
+// after the loop only the cells that reach the bound are read again (a segment of
+// one tile has them in registers) and their elements above it ranked.  Rows whose ties overflow the lists take scan_top.
 template <class Z, int EPT, bool TOP>
 __global__ __launch_bounds__(TW) void token_segment_kernel(const Z* logits, int64_t ld, const float* temperature,
                                                            RowOut r, SegmentPlan pl, Partial* part, uint64_t* tops) {
@@ -268,11 +328,13 @@ __global__ __launch_bounds__(TW) void token_segment_kernel(const Z* logits, int6
   const Z* z = logits + t * ld;
   const float temp = temperature ? temperature[t] : 1.0f;
   const float c = inv_temperature(temp);
+  Given given{-1, 0.0f};
+  if (!part) given = load_given(r, z, t, tid);
   float m = NEG_INF, S = 0.0f, Es = 0.0f, cmax = NEG_INF;
   int cell = 0, in_cell = 0;
+  float x[EPT];
   for (int tile = t0; tile < t1; ++tile) {
     const int64_t j0 = (int64_t)tile * TILE + tid * E;
-    float x[EPT];
     if ((int64_t)(tile + 1) * TILE <= r.V) {
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
@@ -342,20 +404,24 @@ __global__ __launch_bounds__(TW) void token_segment_kernel(const Z* logits, int6
   }
   if constexpr (TOP) {
     const int n = r.top_n;
-    uint32_t key[TW / 64];
+    float v[4];
 #pragma unroll
-    for (int q = 0; q < TW / 64; ++q) key[q] = order_key(tmax[q * 64 + lane]);
-    uint32_t bar = nth_key<KeyShift<Z>::SHIFT>(key, n);
-    bar = bar < KEY_LOWEST ? KEY_LOWEST : bar;
-    for (int i = 0; i < cell; ++i) {
-      if (order_key(cells[i * TW + tid]) >= bar) {
+    for (int q = 0; q < TW / 64; ++q) v[q] = tmax[q * 64 + lane];
+    const float bar = nth_bound<KeyShift<Z>::SHIFT>(v, n);
+    const bool one = t1 - t0 == 1;  // the segment's elements are still in registers
+    if (one) {
+      const int64_t j0 = (int64_t)t0 * TILE + tid * E;
+      push_hits<EPT>(top, bar, x, [&](int e) { return (uint32_t)(j0 + e / E * TW * E + e % E); });
+    }
+    for (int i = 0; i < (one ? 0 : cell); ++i) {
+      if (cells[i * TW + tid] >= bar) {
         const int at = atomicAdd(&ncell, 1);
         if (at < CELL_CAP) list[at] = (uint16_t)(i * TW + tid);
       }
     }
     __syncthreads();
     const int nc = ncell;
-    if (nc <= CELL_CAP) {
+    if (!one && nc <= CELL_CAP) {
       const int per = pl.tpc * NG;
       for (int i = tid; i < nc * per; i += TW) {
         const int ci = list[i / per], q = i % per;
@@ -364,14 +430,7 @@ __global__ __launch_bounds__(TW) void token_segment_kernel(const Z* logits, int6
         if (tile >= t1 || j >= r.V) continue;
         float x[E];
         load_granule(z, j, r.V, x);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const uint32_t k = order_key(x[e]);
-          if (k >= bar && x[e] > NEG_INF) {
-            const int at = atomicAdd(&top.count, 1);
-            if (at < LIST_CAP) top.list[at] = composite(k, (uint32_t)(j + e));
-          }
-        }
+        push_hits<E>(top, bar, x, [&](int e) { return (uint32_t)(j + e); });
       }
       __syncthreads();
     }
@@ -386,7 +445,7 @@ __global__ __launch_bounds__(TW) void token_segment_kernel(const Z* logits, int6
       for (int i = tid; i < n; i += TW) tops[(size_t)blockIdx.x * n + i] = top.sorted[i];
   }
   if (!part) {
-    write_row(r, z, t, temp, M, S, Es, top.sorted, tid, TW);
+    write_row(r, z, t, temp, M, S, Es, top.sorted, given, tid, TW);
   } else if (tid == 0) {
     part[blockIdx.x] = Partial{M, S, Es, 0.0f};
   }
@@ -407,7 +466,7 @@ __global__ __launch_bounds__(TW) void token_join_kernel(const Z* logits, int64_t
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63;
   const int n = r.top_n, total = segs * n;
-  uint32_t key[4];  // of the lists' heads
+  float head[4];  // the lists' heads
   uint64_t v[JOIN_CAP / TW];
   if constexpr (TOP) {
     const uint64_t* const row = tops + (size_t)t * total;
@@ -415,12 +474,14 @@ __global__ __launch_bounds__(TW) void token_join_kernel(const Z* logits, int64_t
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int i = q * 64 + lane;
-      key[q] = i < heads ? comp_key(row[(size_t)(i % segs) * n + i / segs]) : 0;
+      const uint64_t h = i < heads ? row[(size_t)(i % segs) * n + i / segs] : 0;
+      head[q] = h ? key_value(comp_key(h)) : NEG_INF;
     }
 #pragma unroll
     for (int q = 0; q < JOIN_CAP / TW; ++q) v[q] = q * TW + tid < total ? row[q * TW + tid] : 0;
     if (tid == 0) top.count = 0;
   }
+  const Given given = load_given(r, logits + t * ld, t, tid);
   const float temp = temperature ? temperature[t] : 1.0f;
   const float c = inv_temperature(temp);
   // (every wave joins the statistics by itself, in the same order)
@@ -444,16 +505,19 @@ __global__ __launch_bounds__(TW) void token_join_kernel(const Z* logits, int64_t
     Es += __shfl_xor(Es, o);
   }
   if constexpr (TOP) {
-    uint32_t bar = nth_key<KeyShift<Z>::SHIFT>(key, n);
-    bar = bar < KEY_LOWEST ? KEY_LOWEST : bar;
+    const uint32_t bar = order_key(nth_bound<KeyShift<Z>::SHIFT>(head, n));
     __syncthreads();
+    int hits = 0;
+#pragma unroll
+    for (int q = 0; q < JOIN_CAP / TW; ++q) hits += comp_key(v[q]) >= bar;
+    int at = hits ? atomicAdd(&top.count, hits) : 0;
 #pragma unroll
     for (int q = 0; q < JOIN_CAP / TW; ++q)
-      if (comp_key(v[q]) >= bar) top.list[atomicAdd(&top.count, 1)] = v[q];
+      if (comp_key(v[q]) >= bar) top.list[at++] = v[q];
     __syncthreads();
     rank_list(top, n);
   }
-  write_row(r, logits + t * ld, t, temp, m, S, Es, top.sorted, tid, TW);
+  write_row(r, logits + t * ld, t, temp, m, S, Es, top.sorted, given, tid, TW);
 }
 
 // How rows are cut.  Rows that fill the chip by themselves take one workgroup
