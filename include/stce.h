@@ -631,7 +631,8 @@ stce_status stce_fp8_quantize_blocks(const void *x, int32_t dtype, int64_t R, in
  * order; with few output tiles the reduction is cut into segments, summed in
  * order from the workspace: the cut depends on the shapes only, so equal calls
  * give equal bits).  out [M, N] bf16, fp16 or fp32 (rounded once), row stride
- * ldo; with accumulate (fp32 only) the product is added to out.  K = 0 gives
+ * ldo, its extent apart from a's and b's; with accumulate (fp32 only) the
+ * product is added to out.  Scale row strides are at most 2^20.  K = 0 gives
  * zeros; M or N = 0 does nothing. */
 typedef struct stce_block_matmul {
   int64_t M, N, K;

@@ -34,7 +34,7 @@ bool extent_ok(int64_t rows, int64_t ld, size_t es) {
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return x < y + nb && y < x + na;
+  return na && nb && x < y + nb && y < x + na;
 }
 
 size_t bytes_of(int64_t rows, int64_t cols, int64_t ld, size_t es) {
@@ -202,6 +202,10 @@ stce_status stce_fp8_block_matmul(const stce_block_matmul* p, void* ws, size_t w
   if (!is_aligned(p->a, 16) || !is_aligned(p->b, 16) || !is_aligned(p->a_scale, 4) || !is_aligned(p->b_scale, 4) ||
       !is_aligned(p->out, es))
     return fail(STCE_E_ARG, "a and b must be 16-byte aligned, scales and out aligned to their elements");
+  const size_t nout = bytes_of(p->M, p->N, p->ldo, es);
+  if (overlap(p->out, nout, p->a, bytes_of(p->M, p->K, p->lda, 1)) ||
+      overlap(p->out, nout, p->b, bytes_of(p->N, p->K, p->ldb, 1)))
+    return fail(STCE_E_ARG, "out overlaps a or b");
   if ((s = check_ws(ws, ws_bytes, block_matmul_workspace_bytes(*p)))) return s;
   const hipError_t e = launch_block_matmul(*p, ws, (hipStream_t)stream);
   return e ? hip_fail(e, "block matmul") : STCE_OK;

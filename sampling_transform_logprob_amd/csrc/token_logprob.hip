@@ -81,7 +81,9 @@ __device__ void scan_top(const Z* z, int64_t j0, int64_t j1, int n, TopScratch& 
       if (x > NEG_INF && c > cut) s.list[atomicAdd(&s.count, 1)] = c;
     }
     __syncthreads();
-    if (s.count > LIST_CAP - TW) {
+    const bool full = s.count > LIST_CAP - TW;
+    __syncthreads();  // (every thread has read the count before the next step adds to it)
+    if (full) {
       rank_list(s, n);
       for (int i = threadIdx.x; i < n; i += TW) s.list[i] = s.sorted[i];
       if (threadIdx.x == 0) {

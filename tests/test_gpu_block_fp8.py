@@ -216,6 +216,45 @@ def test_linear_layer_and_its_gradients(rng):
     assert np.all(np.abs(y.detach().cpu().numpy() - exact) <= mag * (2.0 ** -3 + 2.0 ** -8) + 1e-3)
 
 
+@pytest.mark.parametrize("T,H,V", [(37, 100, 77), (1, 33, 200), (5, 1, 1), (0, 64, 40)])
+def test_linear_layer_at_odd_sizes(rng, T, H, V):
+    x = torch.from_numpy(rng.standard_normal((T, H)).astype(np.float32)).to(dev()).requires_grad_()
+    w = torch.from_numpy(rng.standard_normal((V, H)).astype(np.float32)).to(dev()).requires_grad_()
+    y = binding.Fp8BlockLinearFunction.apply(x, w)
+    assert y.shape == (T, V)
+    y.sum().backward()                                  # (an expanded gradient: no strides of its own)
+    assert x.grad.shape == x.shape and w.grad.shape == w.shape
+    if T == 0:
+        assert torch.all(w.grad == 0)
+        return
+    xn, wn, gn = x.detach().cpu().numpy(), w.detach().cpu().numpy(), np.ones((T, V), np.float32)
+    q = ref.quantize_blocks
+    for got, (a, sa), (b, sb) in [(y.detach(), q(xn), q(wn, "tile")), (x.grad, q(gn), q(wn, "tile", True)),
+                                  (w.grad, q(gn, "row", True), q(xn, "row", True))]:
+        check_product(got, a, sa, b, sb, "fp32")
+
+
+def test_two_streams_at_once(rng):
+    """The same calls on two streams at the same time: workspaces of their own."""
+    a, sa, b, sb = (torch.from_numpy(x).to(dev()) for x in operands(rng, 20, 500, 4096, "tile"))
+    z = torch.from_numpy(rng.standard_normal((3, 90000)).astype(np.float32)).to(dev())
+    want = binding.fp8_block_matmul(a, sa, b, sb, torch.float32)
+    lse = binding.token_logprobs(z, top_n=30)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    held = [[], []]
+    for _ in range(10):
+        for s, h in zip(streams, held):
+            with torch.cuda.stream(s):
+                h.append((binding.fp8_block_matmul(a, sa, b, sb, torch.float32),
+                          binding.token_logprobs(z, top_n=30, check=False)))
+    torch.cuda.synchronize()
+    for h in held:
+        for o, t in h:
+            assert torch.equal(o, want)
+            assert all(torch.equal(t[k], lse[k]) for k in lse)
+
+
 def test_head_and_token_logprobs_together(rng):
     """hidden -> fp8 head -> log probabilities and entropy -> loss -> gradients,
     as a training step runs them, against fp64 on the same quantized operands."""
@@ -279,6 +318,9 @@ def test_refusals(rng):
         mm(a, sa, b, sb, out=torch.empty(4, 300, dtype=torch.bfloat16, device=dev()), accumulate=True)
     with pytest.raises(ValueError, match="out must be"):
         mm(a, sa, b, sb, out=torch.empty(4, 301, device=dev()))
+    both = torch.zeros(4 * 300 * 4, dtype=torch.uint8, device=dev())
+    with pytest.raises(binding.StceError, match="overlaps"):
+        mm(both[1024:1280].view(4, 64), sa, b, sb, out=both.view(torch.float32).view(4, 300))
 
 
 def test_both_marshalling_paths_agree(rng, monkeypatch):

@@ -130,7 +130,9 @@ def _matmul(**kw):
     (dict(ldo=7), b"ldo=7"), (dict(b_rows=64), b"b_rows=64"), (dict(a_row_stride=-1), b"strides"),
     (dict(accumulate=1, out_dtype=1), b"accumulate"), (dict(a=None), b"required"), (dict(b_scale=None), b"required"),
     (dict(out=None), b"required"), (dict(a=FAKE + 8), b"aligned"), (dict(b_scale=FAKE + 1), b"aligned"),
-    (dict(out=FAKE + 2), b"aligned"),
+    (dict(out=FAKE + 2), b"aligned"), (dict(out=FAKE + 508), b"overlaps"), (dict(out=FAKE - 124), b"overlaps"),
+    (dict(a_row_stride=2**20 + 1), b"at most 2^20"), (dict(M=2**31 - 600, N=2**31 - 600, ldo=2**31), b"ldo="),
+    (dict(M=2**24, N=2**24, ldo=2**24), b"too many"),
 ])
 def test_block_matmul_refusals(lib, kw, msg):
     p = _matmul(**kw)
