@@ -41,23 +41,27 @@ struct TopScratch {
 
 // Keeps the n largest of the list's count entries (count <= LIST_CAP) in
 // sorted[] in decreasing order, zeros past them.  Composites are distinct, so
-// an entry's place is the number of larger ones.  All threads call it;
-// entries are visible to all (a barrier precedes).
+// an entry's place is the number of larger ones, counted by eight lanes.  All
+// threads call it; entries are visible to all (a barrier precedes).
 __device__ inline void rank_list(TopScratch& s, int n) {
-  const int cnt = s.count;
+  constexpr int L = 8;
+  const int cnt = s.count, sub = threadIdx.x % L;
   for (int i = threadIdx.x; i < n; i += TW)
     if (i >= cnt) s.sorted[i] = 0;
-  for (int i = threadIdx.x; i < cnt; i += TW) {
-    const uint64_t mine = s.list[i];
+  // (whole groups of lanes run each pass: the last one's entries past cnt do not count)
+  for (int i = threadIdx.x / L; i < (cnt + TW / L - 1) / (TW / L) * (TW / L); i += TW / L) {
+    const uint64_t mine = i < cnt ? s.list[i] : 0;
     int rank = 0;
-    for (int j = 0; j < cnt; j += 8) {  // (eight reads in flight; what lies past cnt does not count)
-      uint64_t o[8];
+    for (int j = sub; j < cnt; j += 4 * L) {
+      uint64_t o[4];  // (four reads in flight)
 #pragma unroll
-      for (int q = 0; q < 8; ++q) o[q] = s.list[j + q];
+      for (int q = 0; q < 4; ++q) o[q] = s.list[min(j + q * L, LIST_CAP - 1)];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) rank += (j + q < cnt) & (o[q] > mine);
+      for (int q = 0; q < 4; ++q) rank += (j + q * L < cnt) & (o[q] > mine);
     }
-    if (rank < n) s.sorted[rank] = mine;
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) rank += __shfl_xor(rank, o);
+    if (sub == 0 && i < cnt && rank < n) s.sorted[rank] = mine;
   }
   __syncthreads();
 }
