@@ -141,6 +141,29 @@ def test_many_rows(rng, T):
     check(z, tok, temp, 8, out)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("mask", ["ties", "equal", "lowest", "zeros", "columns"])
+def test_tied_rows_of_several_tiles(rng, dtype, mask):
+    """Whole rows in one workgroup, more equal logits than its lists hold."""
+    T, V = 260, 20000
+    say(f"token_logprobs tied rows {mask} {dtype}")
+    z, tok, temp = make(rng, T, V, 2, dtype, {"zeros": "lowest", "columns": None}.get(mask, mask))
+    if mask == "columns":                        # the large logits all in a few threads' places, thousands of them
+        e = 16 // z.element_size()
+        z = torch.where((torch.arange(V) // e) % 256 < 14, z + 20, torch.full_like(z, 1.0))
+    if mask == "zeros":                          # both zeros are one value; a few above them
+        z[:] = 0.0
+        z[:, ::2] = -0.0
+        z[1::2, 7000:7004] = torch.finfo(DT[dtype]).smallest_normal
+        z[2::3, 300:15000:7] = 2.0
+    if mask == "lowest":                         # four tokens left by a mask of the lowest value
+        z[3:] = torch.finfo(DT[dtype]).min
+        z[3:, 9000:9004] = torch.randn(T - 3, 4, generator=torch.Generator().manual_seed(5)).to(z.dtype)
+    for top_n in (20, 128):
+        out = binding.token_logprobs(z.to(dev()), tok.to(dev()), temp.to(dev()), top_n=top_n, ignore_index=IGNORE)
+        check(z, tok, temp, top_n, out)
+
+
 @pytest.mark.parametrize("V", [40, 5000, 70000])
 def test_invalid_rows(rng, V):
     """NaN, +inf, invalid temperatures and tokens: NaN outputs, no alternatives, and the report."""
