@@ -554,7 +554,7 @@ stce_status stce_fp8_quantize_rows(const void *x, int64_t R, int64_t H, uint8_t 
  * Logits are read once; the row maximum, sums and entropy are fp32 (the
  * exponentials taken relative to the running maximum). */
 typedef struct stce_token_problem {
-  int64_t T;      /* rows, 0 <= T <= 2^24 (0: nothing is done) */
+  int64_t T;      /* rows, 0 <= T < 2^24 (0: nothing is done) */
   int64_t V;      /* tokens per row, 1 <= V < 2^31 - 512 */
   int32_t dtype;  /* of the logits: STCE_DT_BF16, STCE_DT_F16 or STCE_DT_F32 */
   int32_t flags;  /* 0 or STCE_PROBLEM_IGNORE_INDEX */
@@ -612,7 +612,7 @@ stce_status stce_token_logprobs_backward(const stce_token_problem *prob, const f
  * product with it is NaN.  Writes codes [Q, round_up(L, 16)] (columns past L
  * zero; row stride ld_codes, a multiple of 16; 16-byte aligned) and scales
  * [ceil(L / 128)][Q or ceil(Q / 128)] fp32, the block index slowest: the
- * operands of stce_fp8_block_matmul.  (The transposed forms are what a weight
+ * operands of stce_fp8_block_matmul; neither may overlap x.  (The transposed forms are what a weight
  * gradient, reduced over tokens, and a hidden gradient, reduced over the
  * vocabulary, take.) */
 #define STCE_QUANT_TILE 1

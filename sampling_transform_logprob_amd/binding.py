@@ -732,6 +732,15 @@ def _token_workspace(T, V, dtype, top_n):
     return nb.value
 
 
+def _given_workspace(workspace, dev):
+    """A caller's workspace (or None) and its bytes."""
+    if workspace is None:
+        return None, 0
+    if workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+    return workspace, workspace.numel()
+
+
 def token_logprobs(logits, tokens=None, temperature=None, *, top_n: int = 0, ignore_index: Optional[int] = None,
                    check: bool = True, workspace: Optional[torch.Tensor] = None):
     """Log probabilities of given tokens under ``logits`` [T, V] (bf16, fp16 or
@@ -764,6 +773,7 @@ def token_logprobs(logits, tokens=None, temperature=None, *, top_n: int = 0, ign
         nb = _token_workspace(T, prob.V, prob.dtype, top_n)
         if nb:
             workspace = torch.empty(nb, dtype=torch.uint8, device=dev)
+    workspace, ws_bytes = _given_workspace(workspace, dev)
     # one allocation for the fp32 outputs: a row costs little more than its calls
     buf = torch.empty(T * (6 + K + top_n), dtype=torch.float32, device=dev)
     out = dict(stats=buf.as_strided((T, 4), (4, 1), 0), lse=buf.as_strided((T,), (1,), 4 * T),
@@ -780,7 +790,7 @@ def token_logprobs(logits, tokens=None, temperature=None, *, top_n: int = 0, ign
     status = torch.empty(1, dtype=torch.int64, device=dev) if check else None
     o = TokenOutputs(*ptrs)
     _call(L.stce_token_logprobs, dev, ctypes.byref(prob), ctypes.byref(o), _ptr(status), _ptr(workspace),
-          0 if workspace is None else workspace.numel())
+          ws_bytes)
     if check:
         _raise_rows(status, "stce_token_logprobs", dict(temperature=keep[2], target=keep[1]))
     return out
@@ -944,7 +954,8 @@ def fp8_block_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, *, out: O
     _check(L.stce_fp8_block_matmul_workspace_bytes(ctypes.byref(p), ctypes.byref(nb)))
     if workspace is None and nb.value:
         workspace = torch.empty(nb.value, dtype=torch.uint8, device=dev)
-    _call(L.stce_fp8_block_matmul, dev, ctypes.byref(p), _ptr(workspace), 0 if workspace is None else workspace.numel())
+    workspace, ws_bytes = _given_workspace(workspace, dev)
+    _call(L.stce_fp8_block_matmul, dev, ctypes.byref(p), _ptr(workspace), ws_bytes)
     return out
 
 

@@ -8,6 +8,9 @@ using namespace stce;
 
 namespace {
 
+// workgroups of a launch: 256 threads each, fewer than 2^32 in all
+constexpr int64_t MAX_WORKGROUPS = (1 << 24) - 1;
+
 bool is_aligned(const void* ptr, size_t a) { return ((uintptr_t)ptr % a) == 0; }
 
 // bytes of an element of a logits / quantizer / output dtype; 0: none
@@ -54,7 +57,8 @@ stce_status check_token_shapes(const stce_token_problem* p) {
     return fail(STCE_E_ARG, "problem.flags=%d: only STCE_PROBLEM_IGNORE_INDEX is known here", (int)p->flags);
   const size_t es = value_size(p->dtype);
   if (!es) return bad_dtype("logits", p->dtype);
-  if (p->T < 0 || p->T > (1 << 24)) return fail(STCE_E_ARG, "T=%lld out of range [0, 2^24]", (long long)p->T);
+  // (a workgroup per row where there are many)
+  if (p->T < 0 || p->T > MAX_WORKGROUPS) return fail(STCE_E_ARG, "T=%lld out of range [0, 2^24)", (long long)p->T);
   if (p->V < 1 || p->V > INT32_MAX - 512)
     return fail(STCE_E_ARG, "V=%lld out of range [1, 2^31-513]", (long long)p->V);
   if (p->ld < p->V || !extent_ok(p->T, p->ld, es))
@@ -98,8 +102,8 @@ stce_status check_matmul_shapes(const stce_block_matmul* p) {
   // (the rows of a tile's scales are addressed with 32-bit byte offsets)
   if (p->a_row_stride > (1 << 20) || p->b_row_stride > (1 << 20))
     return fail(STCE_E_UNSUPPORTED, "scale row strides must be at most 2^20 elements");
-  // (a workgroup forms at least 128 x 128 outputs where there are more than 64 rows)
-  if (ceil_div(p->M, 64) * ceil_div(p->N, 128) > INT32_MAX / 2)
+  // (at least 128 x 128 outputs a workgroup, or all of up to 64 rows)
+  if (ceil_div(p->M, 128) * ceil_div(p->N, 128) > MAX_WORKGROUPS)
     return fail(STCE_E_UNSUPPORTED, "M=%lld x N=%lld has too many output tiles", (long long)p->M, (long long)p->N);
   if (p->accumulate && p->out_dtype != STCE_DT_F32)
     return fail(STCE_E_UNSUPPORTED, "accumulate takes an fp32 output");
@@ -170,7 +174,7 @@ stce_status stce_fp8_quantize_blocks(const void* x, int32_t dtype, int64_t R, in
                 (long long)R, (long long)C);
   if (ld < C || !extent_ok(R, ld, es))
     return fail(STCE_E_ARG, "ld=%lld must be at least C=%lld", (long long)ld, (long long)C);
-  if (ceil_div(R, 128) * ceil_div(C, 128) > INT32_MAX)
+  if (ceil_div(R, 128) * ceil_div(C, 128) > MAX_WORKGROUPS)
     return fail(STCE_E_UNSUPPORTED, "R=%lld x C=%lld has too many blocks for one launch", (long long)R, (long long)C);
   const int64_t L = (flags & STCE_QUANT_TRANSPOSE) ? R : C, Q = (flags & STCE_QUANT_TRANSPOSE) ? C : R;
   if (ld_codes % 16 != 0 || ld_codes < round_up(L, 16) || !extent_ok(Q, ld_codes, 1))
@@ -180,6 +184,11 @@ stce_status stce_fp8_quantize_blocks(const void* x, int32_t dtype, int64_t R, in
   if (!x || !codes || !scales) return fail(STCE_E_ARG, "x, codes and scales are required");
   if (!is_aligned(x, es) || !is_aligned(codes, 16) || !is_aligned(scales, 4))
     return fail(STCE_E_ARG, "x and scales must be aligned to their elements, codes to 16 bytes");
+  const size_t nx = bytes_of(R, C, ld, es);
+  if (overlap(x, nx, codes, bytes_of(Q, round_up(L, 16), ld_codes, 1)) ||
+      overlap(x, nx, scales,
+              4 * (size_t)ceil_div(L, 128) * (size_t)((flags & STCE_QUANT_TILE) ? ceil_div(Q, 128) : Q)))
+    return fail(STCE_E_ARG, "codes or scales overlap x");
   const hipError_t e = launch_quantize_blocks(x, dtype, R, C, ld, flags, codes, ld_codes, scales, (hipStream_t)stream);
   return e ? hip_fail(e, "quantize blocks") : STCE_OK;
 }

@@ -161,6 +161,38 @@ def test_binding_refusals():
         binding.fp8_block_matmul(z, z, z, z)
 
 
+def test_quantize_in_place_is_refused(lib):
+    # x: 4 rows of 32 bf16, stride 40: bytes [FAKE, FAKE + 304); codes 112 bytes at stride 32; scales 16
+    x, v = FAKE, ctypes.c_void_p
+    for codes, scales in [(x, x + 4096), (x - 112, x + 4096), (x + 288, x + 4096), (x + 4096, x),
+                          (x + 4096, x - 12), (x + 4096, x + 300)]:
+        st = lib.stce_fp8_quantize_blocks(v(x), 1, 4, 32, 40, 0, v(codes), 32, v(scales), None)
+        assert st == 1 and b"overlap x" in lib.stce_last_error(), (codes, scales, lib.stce_last_error())
+
+
+def test_launches_of_2_32_threads_are_refused(lib):
+    p, n = _token(T=1 << 24), ctypes.c_size_t()
+    assert lib.stce_token_workspace_bytes(ctypes.byref(p), ctypes.byref(n)) == 1 and b"T=" in lib.stce_last_error()
+    p = _token(T=(1 << 24) - 1)
+    assert lib.stce_token_workspace_bytes(ctypes.byref(p), ctypes.byref(n)) == 0
+    v = ctypes.c_void_p  # 2^12 x 2^12 tiles
+    st = lib.stce_fp8_quantize_blocks(v(FAKE), 1, 2**19, 2**19, 2**19, 0, v(1 << 60), 2**19, v(1 << 61), None)
+    assert st in (1, 2) and b"too many" in lib.stce_last_error()
+    p = _matmul(M=2**19, N=2**19, ldo=2**19)
+    assert lib.stce_fp8_block_matmul_workspace_bytes(ctypes.byref(p), ctypes.byref(n)) == 2
+    assert b"too many" in lib.stce_last_error()
+
+
+def test_workspaces_of_other_kinds_are_refused():
+    cpu = torch.device("cpu")
+    ws = torch.zeros(512, dtype=torch.uint8)
+    assert binding._given_workspace(None, cpu) == (None, 0)
+    assert binding._given_workspace(ws, cpu) == (ws, 512)
+    for bad, dev in ((ws, torch.device("cuda", 0)), (ws.view(torch.float32), cpu), (ws[::2], cpu)):
+        with pytest.raises(ValueError, match="workspace must be"):
+            binding._given_workspace(bad, dev)
+
+
 # ---------------------------------------------------------------------------
 # the oracle against independent definitions
 # ---------------------------------------------------------------------------
