@@ -306,10 +306,16 @@ struct SegmentPlan {
   int tpc;             // tiles per cell (see below)
 };
 
-// Rows from which every row is one workgroup's: one a compute unit (301 x 32,001
-// fp16: 14.6 us against 18.3 us in four segments a row and a joining launch; at
-// 150 x 128,256 bf16 21.5 us in segments against 24.5).
-constexpr int ROWS_FILL = 256;
+// Rows are one workgroup's each where they are short, or from ROWS_A_TILE rows for
+// each tile of 8,192 elements on; other rows are cut into segments, which a second
+// launch joins.  (20 alternatives, bf16, a workgroup a row against segments: 1 x
+// 8,000 6.8 and 9.7 us, 1 x 32,000 9.4 and 9.4, 100 x 32,000 10.1 and 13.6; 8 x
+// 64,000 12.8 and 10.8, 100 x 64,000 13.8 and 15.6; 70 x 128,256 20.1 and 17.7, 130 x
+// 128,256 20.4 and 21.9; 200 x 151,936 22.7 and 26.2.  Without
+// alternatives: 1 x 8,000 4.1 and 5.4, 1 x 32,000 5.9 and 5.4, 100 x 64,000 9.5 and
+// 9.4, 130 x 128,256 15.5 and 15.0.)
+constexpr int SHORT_TILES = 4, ROWS_A_TILE = 8;
+constexpr int ROWS_FILL = 256;  // rows that fill the chip whatever their length
 constexpr int CELLS = 16;      // cells of a thread at most
 constexpr int CELL_CAP = 512;  // cells that may hold alternatives
 
@@ -615,8 +621,8 @@ __global__ __launch_bounds__(TW) void token_join_kernel(const Z* logits, int64_t
   write_row(r, logits + t * ld, t, temp, m, S, Es, top.sorted, given, tid, TW);
 }
 
-// How rows are cut.  Rows that fill the chip by themselves take one workgroup
-// each, tiles of 8,192 elements.  Fewer rows are cut into segments, about 1,024
+// How rows are cut.  Short rows, and rows that fill the chip by themselves, take
+// one workgroup each, tiles of 8,192 elements.  Others are cut into segments, about 1,024
 // workgroups in all (as many as leave a row's segments' alternatives to one
 // joining workgroup), with the smallest tile that makes a segment one tile: all
 // its loads are then in flight at once.
@@ -626,7 +632,9 @@ struct TokenPlan {
 };
 TokenPlan plan_tokens(const stce_token_problem& p) {
   TokenPlan t{};
-  int64_t most = p.T >= ROWS_FILL ? 1 : ceil_div(1024, p.T);
+  const int64_t long_tiles = ceil_div(p.V, 8192);
+  const bool whole = long_tiles <= SHORT_TILES || p.T >= ROWS_FILL || p.T >= ROWS_A_TILE * long_tiles;
+  int64_t most = whole ? 1 : ceil_div(1024, p.T);
   if (most > SEGS_MAX) most = SEGS_MAX;
   if (p.top_n && most > JOIN_CAP / p.top_n) most = JOIN_CAP / p.top_n;
   t.ept = ceil_div(p.V, 2048) <= most ? 8 : ceil_div(p.V, 4096) <= most ? 16 : 32;

@@ -132,6 +132,20 @@ def test_masks(rng, dtype, mask, T, V):
         check(z, tok, temp, top_n, out)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,V", [(2, 32768), (2, 32769), (39, 40960), (40, 40960), (41, 40961), (255, 8193)])
+def test_sizes_about_the_cut_of_rows(rng, dtype, T, V):
+    """Rows of up to four tiles of 8,192, or of eight rows a tile, are one
+    workgroup's; others are cut into segments."""
+    say(f"token_logprobs {dtype} T={T} V={V}")
+    z, tok, temp = make(rng, T, V, 2, dtype, "masked")
+    for pad, top_n in ((0, 20), (1, 0)):
+        z_dev = strided(z, pad)
+        out = binding.token_logprobs(z_dev, tok.to(dev()), temp.to(dev()), top_n=top_n,
+                                     ignore_index=IGNORE)
+        check(z, tok, temp, top_n, out)
+
+
 @pytest.mark.parametrize("T", [700, 5000])
 def test_many_rows(rng, T):
     V = 1203
