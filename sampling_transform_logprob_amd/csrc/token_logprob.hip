@@ -315,7 +315,9 @@ struct SegmentPlan {
 // alternatives: 1 x 8,000 4.1 and 5.4, 1 x 32,000 5.9 and 5.4, 100 x 64,000 9.5 and
 // 9.4, 130 x 128,256 15.5 and 15.0.)
 constexpr int SHORT_TILES = 4, ROWS_A_TILE = 8;
-constexpr int ROWS_FILL = 256;  // rows that fill the chip whatever their length
+// Rows that fill the chip whatever their length (bf16 rows of 1,000,000, a workgroup a
+// row against segments: 300 rows 153 and 124 us, 500 rows 187 and 205).
+constexpr int ROWS_FILL = 384;
 constexpr int CELLS = 16;      // cells of a thread at most
 constexpr int CELL_CAP = 512;  // cells that may hold alternatives
 

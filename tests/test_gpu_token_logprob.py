@@ -146,6 +146,22 @@ def test_sizes_about_the_cut_of_rows(rng, dtype, T, V):
         check(z, tok, temp, top_n, out)
 
 
+@pytest.mark.parametrize("T", [300, 384])
+def test_many_long_rows_are_cut_or_not(T):
+    """300 rows of 49 tiles of 8,192 are cut into segments, 384 are not: the same
+    values either way, from rows repeated in a batch and scored alone."""
+    V = 400000
+    gen = torch.Generator(device=dev()).manual_seed(5)
+    base = torch.randn(3, V, generator=gen, device=dev()).bfloat16()
+    tok = torch.randint(0, V, (3, 2), generator=gen, device=dev())
+    z, tk = base.repeat(T // 3, 1), tok.repeat(T // 3, 1)
+    out = binding.token_logprobs(z, tk, top_n=20)
+    check(base.cpu(), tok.cpu(), None, 20, {k: v[:3] for k, v in out.items()})
+    for v in out.values():
+        v = v.view(T // 3, -1)
+        assert torch.equal(v, v[:1].expand_as(v))
+
+
 @pytest.mark.parametrize("T", [700, 5000])
 def test_many_rows(rng, T):
     V = 1203
